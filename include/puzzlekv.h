@@ -28,7 +28,8 @@
  *   - The caller allocates and frees every device buffer; the library only
  *     borrows them.  It allocates no device memory itself.
  *   - Storage dtype: PUZZLEKV_BF16 (bf16 dense pages and factors, tensor-core
- *     path) or PUZZLEKV_F32 (fp32, CUDA-core path).  Outputs are fp32.
+ *     path) or PUZZLEKV_F32 (fp32, CUDA-core path).  Decode outputs are fp32;
+ *     the chunk calls return kv_dtype.
  *   - Supported shapes: head_dim d in {64, 128}; page size P in {16, 32, 64}
  *     with P <= d; 1 <= rank <= P; query heads per KV head G = Hq / H in
  *     1..8.  Key/value ranks are stored padded to a multiple of 8 (the
@@ -359,6 +360,109 @@ puzzlekv_status puzzlekv_decode_step(puzzlekv_store *store, int32_t layer, const
 puzzlekv_status puzzlekv_decode_attention_static_scratch(puzzlekv_store *store, int32_t layer, const void *q,
                                                          float *out, const int32_t *seq_ids, int32_t B,
                                                          void *stream);
+
+/*
+ * Workspace bytes of puzzlekv_chunk_attention and puzzlekv_append_chunk for
+ * these arguments at the sequences' present lengths (either pointer may be
+ * NULL).  Host-only.
+ */
+puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t layer, const int32_t *seq_ids,
+                                         const int32_t *counts, int32_t B, size_t *attention_bytes,
+                                         size_t *append_bytes);
+
+/*
+ * Attention of a chunk of new tokens per sequence over the hybrid cache and
+ * the chunk itself [PuzzleKV §3.3 ④, eqs. (4)-(5)], for prompts processed in
+ * chunks and for drafted tokens verified together: token j of a sequence that
+ * holds T tokens attends the T cached tokens, in the page kinds of that length,
+ * and tokens 0..j of its chunk, which are dense.  The store is not changed
+ * (puzzlekv_append_chunk adds the chunk afterwards).  Factorized pages are
+ * rebuilt (L R, rounded once to kv_dtype) where many queries share them.
+ *   q:       device, [N][num_q_heads][head_dim] in kv_dtype, N = sum of counts,
+ *            the sequences' tokens one after another in list order;
+ *   k, v:    device, [N][num_kv_heads][head_dim] in kv_dtype (keys before RoPE
+ *            in stores with rope_theta > 0; queries already rotated).  Values
+ *            of a chunk must be finite: an infinity or NaN in the v row of a
+ *            token may reach the outputs of the chunk's earlier tokens.
+ *   out:     device, [N][num_q_heads][head_dim] in kv_dtype.
+ *   seq_ids, counts: host, B distinct slots, empty ones included, and the
+ *            number of new tokens of each, 0 or more; at most
+ *            max_tokens_per_seq with the cached ones.
+ *   work:    device, 256-byte aligned, work_bytes >= what
+ *            puzzlekv_chunk_workspace reports; its contents are scratch.
+ * The call may be captured into a CUDA graph once puzzlekv_wait_background has
+ * been called on the capturing stream; a replay attends the store's content at
+ * the lengths it was captured with.  Graphs that may run at the same time need
+ * workspaces of their own.
+ */
+puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *store, int32_t layer, const void *q, const void *k,
+                                         const void *v, void *out, const int32_t *seq_ids, const int32_t *counts,
+                                         int32_t B, void *work, size_t work_bytes, void *stream);
+
+/*
+ * Append a chunk of tokens per listed sequence to `layer`, any number at once
+ * [PuzzleKV §3.3 ⑤]; an empty slot takes its first tokens this way too.  Rows
+ * that end in the sink or the local window go to the dense pages; every page
+ * that has left the window at the new length is factorized on `stream` (unless
+ * it was converted ahead of time), from the ring or, when the chunk is longer
+ * than the ring, from a copy of its rows in `work`.
+ *   k, v, seq_ids, counts: as puzzlekv_chunk_attention.
+ *   work: as there, sized by puzzlekv_chunk_workspace (NULL if it reports 0).
+ * Equivalent to puzzlekv_append_token once per token.  Cannot be captured.
+ */
+puzzlekv_status puzzlekv_append_chunk(puzzlekv_store *store, int32_t layer, const void *k, const void *v,
+                                      const int32_t *seq_ids, const int32_t *counts, int32_t B, void *work,
+                                      size_t work_bytes, void *stream);
+
+/*
+ * Read rows of the cache as attention sees them: rows starts[i] .. starts[i] +
+ * counts[i] - 1 of each listed sequence, factorized pages rebuilt as L R
+ * (rounded once to kv_dtype), dense rows as stored, keys of stores with
+ * rope_theta > 0 turned at their positions.
+ *   k, v: device, [N][num_kv_heads][head_dim] in kv_dtype, N = sum of counts.
+ */
+puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *store, int32_t layer, const int32_t *seq_ids,
+                                     const int32_t *starts, const int32_t *counts, int32_t B, void *k, void *v,
+                                     void *stream);
+
+/*
+ * Put factors computed elsewhere into the records of pages [page0, page0 + n)
+ * of one sequence and layer (bf16 and fp32 stores): a cache restored or handed
+ * over without its dense rows.  The pages must be complete and past the sink;
+ * records that exist are replaced.  A page inside the local window stays dense
+ * until it leaves the window.
+ *   LK, RK: device, [num_kv_heads][n][P][rank_k] and [num_kv_heads][n][rank_k][head_dim];
+ *   LV, RV: the same with rank_v; kv_dtype.
+ * Cannot be captured.
+ */
+puzzlekv_status puzzlekv_load_factors(puzzlekv_store *store, int32_t layer, int32_t seq, int32_t page0, int32_t n,
+                                      const void *LK, const void *RK, const void *LV, const void *RV, void *stream);
+
+/*
+ * Copy whole sequences (every layer: factor records, dense pages, page table,
+ * bookkeeping) between slots of the store, all pairs at once: slot dst_ids[i]
+ * becomes what slot src_ids[i] was before the call, so permutations and
+ * cycles are allowed (reordered beams), and a source may appear several times
+ * (forks).  A destination's earlier content is dropped; a source that is no
+ * destination keeps its own.
+ *   src_ids, dst_ids: host, n entries in [1, 64]; destinations distinct,
+ *            sources holding tokens, with equal lengths in all layers.
+ * Orders `stream` after all pending background work.  Cannot be captured.
+ */
+puzzlekv_status puzzlekv_copy_sequences(puzzlekv_store *store, const int32_t *src_ids, const int32_t *dst_ids,
+                                        int32_t n, void *stream);
+
+/*
+ * Cut the listed sequences back to lengths[i] tokens in every layer (rejected
+ * drafts); length 0 empties the slot.  Pages that the shorter length makes
+ * dense again must still be in the dense ring: going back page_size tokens or
+ * fewer from the longest length since the prompt always is possible where the
+ * prompt itself is not cut; otherwise PUZZLEKV_ERR_INVALID_ARG, with nothing
+ * changed.  Orders `stream` after all pending background work.  Cannot be
+ * captured.
+ */
+puzzlekv_status puzzlekv_truncate_sequences(puzzlekv_store *store, const int32_t *seq_ids, const int32_t *lengths,
+                                            int32_t B, void *stream);
 
 /*
  * Host-side accounting of one (sequence, layer) from the store's host mirror

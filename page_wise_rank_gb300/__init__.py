@@ -80,6 +80,12 @@ def _seq_ids(seq_ids: Sequence[int]):
     return arr, len(key)
 
 
+def _ints(values: Sequence[int], n: int, name: str):
+    if len(values) != n:
+        raise ValueError(f"{name} must have {n} entries, got {len(values)}")
+    return (ctypes.c_int32 * max(n, 1))(*[int(v) for v in values])
+
+
 def query_sizes(cfg: StoreConfig) -> dict:
     """Byte sizes of the dense pool, factor pool, page table and workspace."""
     s = [ctypes.c_size_t() for _ in range(4)]
@@ -296,6 +302,123 @@ class Store:
         check(lib().puzzlekv_decode_attention_static_scratch(self._h, layer, _ptr(q), _ptr(out), ids, B,
                                                              _stream(stream)))
         return out
+
+    def _on(self, stream):
+        """Context of a chunk call: the store's device, and `stream` (default: the device's
+        current one) as torch's current stream, so that what the call allocates belongs to it."""
+        if stream is not None:
+            return torch.cuda.stream(stream)
+        return torch.cuda.device(self.dense_pool.device)
+
+    def _need_here(self, t: torch.Tensor, shape, name: str) -> None:
+        _need(t, shape, self.cfg.kv_dtype, name)
+        if t.device != self.dense_pool.device:
+            raise ValueError(f"{name} is on {t.device}, the store on {self.dense_pool.device}")
+
+    def _scratch(self, nbytes: int) -> torch.Tensor:
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.dense_pool.device)
+
+    def chunk_workspace(self, layer: int, seq_ids: Sequence[int], counts: Sequence[int]) -> dict:
+        """Workspace bytes of chunk_attention and append_chunk at the present lengths."""
+        ids, B = _seq_ids(seq_ids)
+        a, b = ctypes.c_size_t(), ctypes.c_size_t()
+        check(lib().puzzlekv_chunk_workspace(self._h, layer, ids, _ints(counts, B, "counts"), B, ctypes.byref(a),
+                                             ctypes.byref(b)))
+        return {"attention": a.value, "append": b.value}
+
+    def chunk_attention(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_ids: Sequence[int],
+                        counts: Sequence[int], out: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of a chunk of new tokens per sequence over the cache and, causally, the
+        chunk (§3.3 ④): q [N, Hq, d], k, v [N, H, d], N = sum(counts), sequences one after another.
+        Returns out [N, Hq, d] in kv_dtype; the store is unchanged (append_chunk adds the chunk).
+        `workspace` (uint8, of chunk_workspace's size) is allocated if not given."""
+        c = self.cfg
+        ids, B = _seq_ids(seq_ids)
+        cnt = _ints(counts, B, "counts")
+        N = sum(cnt[:B])
+        self._need_here(q, (N, c.num_q_heads, c.head_dim), "q")
+        self._need_here(k, (N, c.num_kv_heads, c.head_dim), "k")
+        self._need_here(v, (N, c.num_kv_heads, c.head_dim), "v")
+        with self._on(stream):
+            nb = ctypes.c_size_t()
+            check(lib().puzzlekv_chunk_workspace(self._h, layer, ids, cnt, B, ctypes.byref(nb), None))
+            if out is None:
+                out = torch.empty_like(q)
+            else:
+                self._need_here(out, (N, c.num_q_heads, c.head_dim), "out")
+            if N == 0:
+                return out
+            work = workspace if workspace is not None else self._scratch(nb.value)
+            check(lib().puzzlekv_chunk_attention(self._h, layer, _ptr(q), _ptr(k), _ptr(v), _ptr(out), ids, cnt, B,
+                                                 _ptr(work), work.numel() * work.element_size(), _stream(stream)))
+        return out
+
+    def append_chunk(self, layer: int, k: torch.Tensor, v: torch.Tensor, seq_ids: Sequence[int],
+                     counts: Sequence[int], stream=None) -> None:
+        """Append counts[i] tokens to each sequence (empty slots included) of `layer`: k, v
+        [N, H, d]; pages that leave the window are factorized (§3.3 ⑤)."""
+        c = self.cfg
+        ids, B = _seq_ids(seq_ids)
+        cnt = _ints(counts, B, "counts")
+        N = sum(cnt[:B])
+        self._need_here(k, (N, c.num_kv_heads, c.head_dim), "k")
+        self._need_here(v, (N, c.num_kv_heads, c.head_dim), "v")
+        with self._on(stream):
+            nb = ctypes.c_size_t()
+            check(lib().puzzlekv_chunk_workspace(self._h, layer, ids, cnt, B, None, ctypes.byref(nb)))
+            if N == 0:
+                return
+            work = self._scratch(nb.value) if nb.value else None
+            check(lib().puzzlekv_append_chunk(self._h, layer, _ptr(k), _ptr(v), ids, cnt, B,
+                                              _ptr(work) if work is not None else None, nb.value, _stream(stream)))
+
+    def read_tokens(self, layer: int, seq_ids: Sequence[int], starts: Sequence[int], counts: Sequence[int],
+                    stream=None) -> tuple:
+        """Rows [starts[i], starts[i] + counts[i]) of each sequence as attention sees them
+        (factorized pages as L R): (k, v), each [N, H, d] in kv_dtype."""
+        c = self.cfg
+        ids, B = _seq_ids(seq_ids)
+        st, cnt = _ints(starts, B, "starts"), _ints(counts, B, "counts")
+        if any(n < 0 or n > c.max_tokens_per_seq for n in cnt[:B]):  # before anything of that size is allocated
+            raise ValueError("counts must be in [0, max_tokens_per_seq]")
+        N = sum(cnt[:B])
+        with self._on(stream):
+            k = torch.empty(max(N, 1), c.num_kv_heads, c.head_dim, dtype=c.kv_dtype, device=self.dense_pool.device)
+            v = torch.empty_like(k)
+            check(lib().puzzlekv_read_tokens(self._h, layer, ids, st, cnt, B, _ptr(k), _ptr(v), _stream(stream)))
+        return k[:N], v[:N]
+
+    def load_factors(self, layer: int, seq: int, page0: int, LK: torch.Tensor, RK: torch.Tensor, LV: torch.Tensor,
+                     RV: torch.Tensor, stream=None) -> None:
+        """Factors computed elsewhere into the records of pages page0 .. page0 + n - 1: LK [H, n, P, rk],
+        RK [H, n, rk, d], LV [H, n, P, rv], RV [H, n, rv, d] in kv_dtype (bf16 and fp32 stores)."""
+        c = self.cfg
+        if LK.dim() != 4:
+            raise ValueError("LK must be [H, n, P, rank_k]")
+        H, n, P, d = c.num_kv_heads, LK.shape[1], c.page_size, c.head_dim
+        self._need_here(LK, (H, n, P, c.rank_k), "LK")
+        self._need_here(RK, (H, n, c.rank_k, d), "RK")
+        self._need_here(LV, (H, n, P, c.rank_v), "LV")
+        self._need_here(RV, (H, n, c.rank_v, d), "RV")
+        with self._on(stream):
+            check(lib().puzzlekv_load_factors(self._h, layer, seq, page0, n, _ptr(LK), _ptr(RK), _ptr(LV), _ptr(RV),
+                                              _stream(stream)))
+
+    def copy_sequences(self, src_ids: Sequence[int], dst_ids: Sequence[int], stream=None) -> None:
+        """Slot dst_ids[i] becomes what slot src_ids[i] was before the call, all pairs at once
+        (forks, reordered beams, compaction); every layer."""
+        n = len(dst_ids)
+        with self._on(stream):
+            check(lib().puzzlekv_copy_sequences(self._h, _ints(src_ids, n, "src_ids"), _ints(dst_ids, n, "dst_ids"), n,
+                                                _stream(stream)))
+
+    def truncate_sequences(self, seq_ids: Sequence[int], lengths: Sequence[int], stream=None) -> None:
+        """Cut sequences back to lengths[i] tokens in every layer (0 empties the slot); the pages
+        that become dense again must still be in the dense ring."""
+        ids, B = _seq_ids(seq_ids)
+        with self._on(stream):
+            check(lib().puzzlekv_truncate_sequences(self._h, ids, _ints(lengths, B, "lengths"), B, _stream(stream)))
 
     def stats(self, seq: int, layer: int) -> dict:
         n = ctypes.c_int32()

@@ -34,6 +34,13 @@ EXPORTED = (
     "puzzlekv_decode_step",
     "puzzlekv_convert_ready_pages",
     "puzzlekv_decode_attention_static_scratch",
+    "puzzlekv_chunk_workspace",
+    "puzzlekv_chunk_attention",
+    "puzzlekv_append_chunk",
+    "puzzlekv_read_tokens",
+    "puzzlekv_load_factors",
+    "puzzlekv_copy_sequences",
+    "puzzlekv_truncate_sequences",
     "puzzlekv_store_stats",
     "puzzlekv_debug_fail_next_wait",
     "puzzlekv_check_device_status",
@@ -89,6 +96,13 @@ def lib() -> ctypes.CDLL:
         "puzzlekv_decode_attention_static_scratch": ([vp, i32, vp, vp, i32p, i32, vp], i32),
         "puzzlekv_decode_step": ([vp, i32, vp, vp, vp, vp, i32p, i32, vp], i32),
         "puzzlekv_convert_ready_pages": ([vp, vp], i32),
+        "puzzlekv_chunk_workspace": ([vp, i32, i32p, i32p, i32, szp, szp], i32),
+        "puzzlekv_chunk_attention": ([vp, i32, vp, vp, vp, vp, i32p, i32p, i32, vp, sz, vp], i32),
+        "puzzlekv_append_chunk": ([vp, i32, vp, vp, i32p, i32p, i32, vp, sz, vp], i32),
+        "puzzlekv_read_tokens": ([vp, i32, i32p, i32p, i32p, i32, vp, vp, vp], i32),
+        "puzzlekv_load_factors": ([vp, i32, i32, i32, i32, vp, vp, vp, vp, vp], i32),
+        "puzzlekv_copy_sequences": ([vp, i32p, i32p, i32, vp], i32),
+        "puzzlekv_truncate_sequences": ([vp, i32p, i32p, i32, vp], i32),
         "puzzlekv_store_stats": ([vp, i32, i32, i32p, i64p, i64p, i64p], i32),
         "puzzlekv_debug_fail_next_wait": ([vp, i32, i64], i32),
         "puzzlekv_check_device_status": ([vp, vp], i32),

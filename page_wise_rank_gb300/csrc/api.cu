@@ -17,11 +17,10 @@
 #include <cmath>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "../../include/puzzlekv.h"
 #include "kernels.h"
 #include "layout.h"
+#include "store.h"
 
 using namespace pkv;
 
@@ -29,7 +28,9 @@ namespace {
 
 thread_local std::string g_last_error;
 
-puzzlekv_status fail(puzzlekv_status st, const char *fmt, ...) {
+}  // namespace
+
+puzzlekv_status pkv::fail(puzzlekv_status st, const char *fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -39,11 +40,12 @@ puzzlekv_status fail(puzzlekv_status st, const char *fmt, ...) {
     return st;
 }
 
-puzzlekv_status cuda_fail(cudaError_t e, const char *what) {
+puzzlekv_status pkv::cuda_fail(cudaError_t e, const char *what) {
     return fail(PUZZLEKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
+
 bool aligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 
 int sm_count() {
@@ -113,63 +115,12 @@ void layout_from(Layout &y, const puzzlekv_config *c) {
                 c->factor_int4, c->rope_theta);
 }
 
-// An NVTX range around a call of the C ABI, seen by profilers (free when
-// none is attached).
-struct NvtxRange {
-    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-    NvtxRange(const NvtxRange &) = delete;
-    NvtxRange &operator=(const NvtxRange &) = delete;
-};
-
 }  // namespace
-
-struct puzzlekv_store {
-    puzzlekv_config cfg;
-    Layout y;
-    char *dense_pool, *factor_pool, *page_table, *workspace;
-    std::vector<int> len;    // host mirror [seq][layer]; -1 = empty slot
-    // Which pages have factor records, per (seq, layer): every page in
-    // [sink_pages, conv_upto) and, above it, the pages marked in `marked`
-    // (factorized out of order by a page-list call).
-    std::vector<int> conv_upto;                   // [seq][layer]
-    std::vector<std::vector<uint8_t>> marked;     // [seq][layer][page], allocated on first use
-    std::vector<int2> job_host;  // staging of the batched-conversion job list
-    bool after_decode = false;   // the store's latest launch was a decode launch
-    int fail_next = 0;           // failure-path test hook for the next decode launch (0 = off)
-    uint64_t fail_wait_ns = 0;   // its waits' limit
-    int num_sms;
-    // Batched conversions run on an internal low-priority stream.  A batch's
-    // factor records are first read when one of its pages becomes
-    // factorized, i.e. when its sequence reaches deadline[seq] tokens; the
-    // first call that attends at or past that length makes the caller's
-    // stream wait for the batch.
-    struct ConvBatch {
-        cudaEvent_t done = nullptr;
-        bool pending = false;
-        std::vector<int> deadline;  // [seq]: length at which the batch's first page is factorized
-        std::vector<char> uses;     // [seq][layer]: the batch writes factor records of that layer
-    };
-    cudaStream_t conv_stream = nullptr;
-    cudaEvent_t conv_ready = nullptr;  // caller's stream position a batch starts after
-    std::vector<ConvBatch> batches;    // ring
-    int next_batch = 0;
-    ~puzzlekv_store() {
-        if (conv_stream) cudaStreamSynchronize(conv_stream);
-        for (auto &cb : batches)
-            if (cb.done) cudaEventDestroy(cb.done);
-        if (conv_ready) cudaEventDestroy(conv_ready);
-        if (conv_stream) cudaStreamDestroy(conv_stream);
-    }
-};
 
 constexpr int kConvBatches = 8;
 
-// Make `strm` wait for every pending background conversion batch that the
-// listed sequences (at the given lengths) reach, or for all of them when
-// `all` is set.  Returns true if a wait was inserted.
-static bool wait_conversions(puzzlekv_store *s, cudaStream_t strm, const int32_t *seq_ids, const int *lens, int B,
-                             bool all = false) {
+bool pkv::wait_conversions(puzzlekv_store *s, cudaStream_t strm, const int32_t *seq_ids, const int *lens, int B,
+                           bool all) {
     bool waited = false;
     for (auto &cb : s->batches) {
         if (!cb.pending) continue;
@@ -228,32 +179,6 @@ static cudaError_t end_batch(puzzlekv_store *s, puzzlekv_store::ConvBatch &cb) {
     return e;
 }
 
-static int *lengths_ptr(puzzlekv_store *s) { return reinterpret_cast<int *>(s->page_table); }
-static int *desc_ptr(puzzlekv_store *s) { return reinterpret_cast<int *>(s->page_table + s->y.desc_offset); }
-static int *status_ptr(puzzlekv_store *s) { return reinterpret_cast<int *>(s->workspace); }
-
-// Factor-record bookkeeping of (seq b, layer l).
-static bool has_factors(const puzzlekv_store *s, int b, int l, int p) {
-    const size_t i = (size_t)b * s->y.L + l;
-    if (p < s->conv_upto[i]) return p >= s->y.sink_pages;
-    const std::vector<uint8_t> &m = s->marked[i];
-    return (size_t)p < m.size() && m[p] != 0;
-}
-static void set_factors(puzzlekv_store *s, int b, int l, int p) {
-    const size_t i = (size_t)b * s->y.L + l;
-    int &upto = s->conv_upto[i];
-    std::vector<uint8_t> &m = s->marked[i];
-    if (p < upto) return;
-    if (m.size() < (size_t)s->y.n_pg_max) m.assign(s->y.n_pg_max, 0);
-    m[p] = 1;
-    while (upto < s->y.n_pg_max && m[upto]) m[upto++] = 0;  // extend the prefix over marked pages
-}
-static void reset_factors(puzzlekv_store *s, int b, int l, int upto) {
-    const size_t i = (size_t)b * s->y.L + l;
-    s->conv_upto[i] = upto;
-    std::vector<uint8_t>().swap(s->marked[i]);
-}
-
 extern "C" {
 
 const char *puzzlekv_last_error(void) { return g_last_error.c_str(); }
@@ -306,6 +231,7 @@ puzzlekv_status puzzlekv_store_create(const puzzlekv_config *cfg, void *dense_po
     s->len.assign((size_t)cfg->max_batch * cfg->num_layers, -1);
     s->conv_upto.assign((size_t)cfg->max_batch * cfg->num_layers, 0);
     s->marked.resize((size_t)cfg->max_batch * cfg->num_layers);
+    s->dense_lo.assign((size_t)cfg->max_batch * cfg->num_layers, s->y.sink_pages);
     s->num_sms = sm_count();
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemsetAsync(dense_pool, 0, s->y.dense_pool_bytes, strm);
@@ -431,6 +357,7 @@ static puzzlekv_status prefill(puzzlekv_store *s, int32_t seq, int32_t layer0, i
     for (int l = layer0; l < layer0 + n_layers; ++l) {
         s->len[(size_t)seq * y.L + l] = T;
         reset_factors(s, seq, l, f_lo >= 0 ? f_hi : y.sink_pages);
+        s->dense_lo[(size_t)seq * y.L + l] = f_lo >= 0 ? f_hi : y.sink_pages;
     }
     return PUZZLEKV_OK;
 }
@@ -661,7 +588,7 @@ puzzlekv_status puzzlekv_append_token(puzzlekv_store *s, int32_t layer, const vo
         s->after_decode = false;
         if (e != cudaSuccess) return cuda_fail(e, "conversion launch");
     }
-    for (int i = 0; i < B; ++i) s->len[(size_t)seq_ids[i] * y.L + layer] += 1;
+    for (int i = 0; i < B; ++i) grow_dense(s, seq_ids[i], layer, s->len[(size_t)seq_ids[i] * y.L + layer] += 1);
     return PUZZLEKV_OK;
 }
 
@@ -741,7 +668,7 @@ puzzlekv_status puzzlekv_decode_step(puzzlekv_store *s, int32_t layer, const voi
     e = launch_decode(dp, total, max_pages, s->num_sms, strm);
     if (e != cudaSuccess) return cuda_fail(e, "decode step launch");
     s->after_decode = true;
-    for (int i = 0; i < B; ++i) s->len[(size_t)seq_ids[i] * y.L + layer] += 1;
+    for (int i = 0; i < B; ++i) grow_dense(s, seq_ids[i], layer, s->len[(size_t)seq_ids[i] * y.L + layer] += 1);
     return PUZZLEKV_OK;
 }
 

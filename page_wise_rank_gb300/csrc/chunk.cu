@@ -1,0 +1,207 @@
+// Attention of a chunk of query tokens over densely laid out keys and values
+// in CUDA-core fp32 arithmetic, and the merge of split softmax states
+// ("PuzzleKV: Page-Wise Low-Rank Decomposition for KV Cache Compression",
+// §3.3 ④, eq. (5)).
+//
+// With m the running maximum (log2 units) of a row's scores s = q k / sqrt(d),
+//   l = sum 2^(s - m),  o = sum 2^(s - m) v,  out = o / l,
+// one pass over the keys; query token j of a sequence with T cached tokens
+// sees keys 0 .. T + j.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace pkv {
+
+constexpr int CS_ROWS = 32, CS_KEYS = 32;  // query rows and keys of a tile
+
+// Block (tile of 32 query rows of one (entry, KV head), split): 128 threads,
+// eight to a pair of rows.  A thread scores 2 rows x 4 keys and accumulates
+// 2 rows x D/8 columns, so that a shared-memory vector feeds two rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams p) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int PQ = D + 4;  // row pitch: the four row groups of a warp start on distinct banks
+    float *Qs = sm, *Ks = Qs + CS_ROWS * PQ, *Vs = Ks + CS_KEYS * PQ, *Ps = Vs + CS_KEYS * PQ;
+    const int tid = threadIdx.x, tx = tid & 7, ty = tid >> 3;
+    int i = 0;
+    while ((int)blockIdx.x >= p.tile_off[i + 1]) ++i;
+    const int G = p.G, R = p.n[i] * G, tiles = (R + CS_ROWS - 1) / CS_ROWS, ns = p.ns[i];
+    int u = (int)blockIdx.x - p.tile_off[i];
+    const int sp = u % ns;
+    u /= ns;
+    const int h = u / tiles, row0 = (u % tiles) * CS_ROWS;
+    const int Tk = p.T[i] + p.n[i], nkb = (Tk + CS_KEYS - 1) / CS_KEYS;
+    const int kb0 = (int)((long long)nkb * sp / ns), kb1 = (int)((long long)nkb * (sp + 1) / ns);
+    const T *q = reinterpret_cast<const T *>(p.q);
+    for (int e = tid; e < CS_ROWS * D; e += 128) {
+        const int r = row0 + e / D, c = e % D;
+        Qs[(e / D) * PQ + c] =
+            r < R ? p.scale_log2 * Elem<T>::load(q + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D + c) : 0.f;
+    }
+    int lim[2];  // last key each of the thread's rows sees (-1: no such row)
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][D / 8];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+        const int r = row0 + 2 * ty + a;
+        lim[a] = r < R ? p.T[i] + r / G : -1;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) o[a][c] = 0.f;
+    }
+    const int last_key = p.T[i] + (min(row0 + CS_ROWS, R) - 1) / G;
+    const T *K = reinterpret_cast<const T *>(p.K) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
+    const T *V = reinterpret_cast<const T *>(p.V) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
+    for (int kb = kb0; kb < kb1 && kb * CS_KEYS <= last_key; ++kb) {
+        __syncthreads();
+        for (int e = tid; e < CS_KEYS * D; e += 128) {
+            const int k = e / D, c = e % D, t = kb * CS_KEYS + k;
+            Ks[k * PQ + c] = t < Tk ? Elem<T>::load(K + (size_t)t * p.H * D + c) : 0.f;
+            Vs[k * PQ + c] = t < Tk ? Elem<T>::load(V + (size_t)t * p.H * D + c) : 0.f;
+        }
+        __syncthreads();
+        float s[2][4] = {};
+        for (int c = 0; c < D; c += 4) {
+            float4 qa = *reinterpret_cast<const float4 *>(Qs + (2 * ty) * PQ + c);
+            float4 qb = *reinterpret_cast<const float4 *>(Qs + (2 * ty + 1) * PQ + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 kv = *reinterpret_cast<const float4 *>(Ks + (tx + 8 * j) * PQ + c);
+                s[0][j] = fmaf(qa.x, kv.x, fmaf(qa.y, kv.y, fmaf(qa.z, kv.z, fmaf(qa.w, kv.w, s[0][j]))));
+                s[1][j] = fmaf(qb.x, kv.x, fmaf(qb.y, kv.y, fmaf(qb.z, kv.z, fmaf(qb.w, kv.w, s[1][j]))));
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (kb * CS_KEYS + tx + 8 * j > lim[a]) s[a][j] = -INFINITY;
+                mx = fmaxf(mx, s[a][j]);
+            }
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            const float mn = fmaxf(m[a], mx), base = mn == -INFINITY ? 0.f : mn;
+            const float f = exp2f(m[a] - base);
+            float ls = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float w = exp2f(s[a][j] - base);
+                ls += w;
+                Ps[(2 * ty + a) * (CS_KEYS + 1) + tx + 8 * j] = w;
+            }
+            l[a] = fmaf(l[a], f, ls);
+            m[a] = mn;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) o[a][c] *= f;
+        }
+        __syncwarp();  // a row's eight threads share a warp
+        for (int k = 0; k < CS_KEYS; ++k) {
+            const int t = kb * CS_KEYS + k;
+            float w[2];
+#pragma unroll
+            for (int a = 0; a < 2; ++a) w[a] = Ps[(2 * ty + a) * (CS_KEYS + 1) + k];
+#pragma unroll
+            for (int c4 = 0; c4 < D / 32; ++c4) {
+                const float4 v = *reinterpret_cast<const float4 *>(Vs + k * PQ + 32 * c4 + 4 * tx);
+#pragma unroll
+                for (int a = 0; a < 2; ++a)
+                    if (t <= lim[a]) {  // a key the row does not see adds nothing, whatever its value holds
+                        o[a][4 * c4] = fmaf(w[a], v.x, o[a][4 * c4]);
+                        o[a][4 * c4 + 1] = fmaf(w[a], v.y, o[a][4 * c4 + 1]);
+                        o[a][4 * c4 + 2] = fmaf(w[a], v.z, o[a][4 * c4 + 2]);
+                        o[a][4 * c4 + 3] = fmaf(w[a], v.w, o[a][4 * c4 + 3]);
+                    }
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) l[a] += __shfl_xor_sync(0xffffffffu, l[a], x);
+        const int r = row0 + 2 * ty + a;
+        if (r >= R) continue;
+        if (ns == 1) {
+            const float il = 1.f / l[a];
+            T *dst = reinterpret_cast<T *>(p.out) + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) dst[32 * (c / 4) + 4 * tx + c % 4] = Elem<T>::from_f32(o[a][c] * il);
+        } else {
+            float *row = p.partials + (size_t)(p.poff[i] + (long long)(h * ns + sp) * R + r) * (D + 4);
+            if (tx == 0) *reinterpret_cast<float4 *>(row) = make_float4(m[a], l[a], 0.f, 0.f);
+#pragma unroll
+            for (int c4 = 0; c4 < D / 32; ++c4)
+                *reinterpret_cast<float4 *>(row + 4 + 32 * c4 + 4 * tx) =
+                    make_float4(o[a][4 * c4], o[a][4 * c4 + 1], o[a][4 * c4 + 2], o[a][4 * c4 + 3]);
+        }
+    }
+}
+
+// Warp per query row of an entry with several splits: the states joined in
+// split order (the same sums whatever the launch), eq. (5).
+template <typename T, int D>
+__global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkAttnParams p) {
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    int i = 0;
+    while (i < p.nseq && w >= p.tile_off[i + 1]) ++i;
+    if (i >= p.nseq) return;
+    const int G = p.G, R = p.n[i] * G, ns = p.ns[i];
+    const int u = (int)(w - p.tile_off[i]), h = u / R, r = u % R;
+    const float *rows = p.partials + (size_t)(p.poff[i] + (long long)h * ns * R + r) * (D + 4);
+    const size_t pitch = (size_t)R * (D + 4);
+    float M = -INFINITY;
+    for (int s = lane; s < ns; s += 32) M = fmaxf(M, rows[s * pitch]);
+    M = warp_max(M);
+    constexpr int V = D / 32;
+    float L = 0.f, acc[V] = {};
+    for (int s = 0; s < ns; ++s) {
+        const float *row = rows + s * pitch;
+        const float c = exp2f(row[0] - M);
+        L = fmaf(c, row[1], L);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(c, row[4 + lane * V + k], acc[k]);
+    }
+    const float il = 1.f / L;
+    T *dst = reinterpret_cast<T *>(p.out) + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D;
+#pragma unroll
+    for (int k = 0; k < V; ++k) dst[lane * V + k] = Elem<T>::from_f32(acc[k] * il);
+}
+
+template <typename T, int D>
+static cudaError_t simple_t(ChunkAttnParams &p, cudaStream_t st) {
+    constexpr int smem = ((CS_ROWS + 2 * CS_KEYS) * (D + 4) + CS_ROWS * (CS_KEYS + 1)) * 4;
+    cudaError_t e = cudaFuncSetAttribute(chunk_simple_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    chunk_simple_kernel<T, D><<<(unsigned)p.tile_off[p.nseq], 128, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_simple(ChunkAttnParams &p, int dtype, cudaStream_t st) {
+    p.tile_off[0] = 0;
+    for (int i = 0; i < p.nseq; ++i)
+        p.tile_off[i + 1] = p.tile_off[i] + p.H * ((p.n[i] * p.G + CS_ROWS - 1) / CS_ROWS) * p.ns[i];
+    if (p.tile_off[p.nseq] == 0) return cudaSuccess;
+    if (dtype == 1) return p.d == 64 ? simple_t<__nv_bfloat16, 64>(p, st) : simple_t<__nv_bfloat16, 128>(p, st);
+    return p.d == 64 ? simple_t<float, 64>(p, st) : simple_t<float, 128>(p, st);
+}
+
+cudaError_t launch_chunk_merge(const ChunkAttnParams &q, int dtype, cudaStream_t st) {
+    ChunkAttnParams p = q;
+    p.tile_off[0] = 0;
+    for (int i = 0; i < p.nseq; ++i) p.tile_off[i + 1] = p.tile_off[i] + (p.ns[i] > 1 ? p.H * p.n[i] * p.G : 0);
+    const int rows = p.tile_off[p.nseq];
+    if (rows == 0) return cudaSuccess;
+    const unsigned grid = (unsigned)((rows + 3) / 4);
+    if (dtype == 1) {
+        if (p.d == 64) chunk_merge_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
+        else chunk_merge_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p);
+    } else {
+        if (p.d == 64) chunk_merge_kernel<float, 64><<<grid, 128, 0, st>>>(p);
+        else chunk_merge_kernel<float, 128><<<grid, 128, 0, st>>>(p);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace pkv

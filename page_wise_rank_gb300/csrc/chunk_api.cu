@@ -1,0 +1,596 @@
+// C ABI of the calls that work on several tokens or whole sequences at once
+// (declared in include/puzzlekv.h): chunk attention, chunk append, reading
+// rows, loading factors, copying and cutting back sequences.  Every argument
+// is checked on the host before anything is launched, the host mirror decides
+// which pages are dense, and scratch memory is the caller's.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <exception>
+#include <vector>
+
+#include "../../include/puzzlekv.h"
+#include "kernels.h"
+#include "layout.h"
+#include "store.h"
+
+using namespace pkv;
+
+namespace {
+
+// Run an entry point's body; a C++ exception (host memory) becomes a status.
+template <typename F>
+puzzlekv_status guarded(F body) {
+    try {
+        return body();
+    } catch (const std::exception &e) {
+        return fail(PUZZLEKV_ERR_INVALID_ARG, "host-side failure: %s", e.what());
+    } catch (...) {
+        return fail(PUZZLEKV_ERR_INVALID_ARG, "host-side failure");
+    }
+}
+
+int length_of(const puzzlekv_store *s, int b, int l) { return std::max(0, s->len[(size_t)b * s->y.L + l]); }
+
+// A call that changes the host mirror cannot be captured: a replay would
+// repeat the device work without the bookkeeping.
+puzzlekv_status refuse_capture(cudaStream_t strm) {
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(strm, &c);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (c != cudaStreamCaptureStatusNone)
+        return fail(PUZZLEKV_ERR_UNSUPPORTED, "this call changes the store's host state and cannot be captured");
+    return PUZZLEKV_OK;
+}
+
+puzzlekv_status check_list(const puzzlekv_store *s, const int32_t *ids, int32_t B, const char *what) {
+    if (!s) return fail(PUZZLEKV_ERR_INVALID_ARG, "store is NULL");
+    if (B < 1 || B > MAX_CALL_BATCH) return fail(PUZZLEKV_ERR_INVALID_ARG, "B must be in [1, %d]", MAX_CALL_BATCH);
+    if (!ids) return fail(PUZZLEKV_ERR_INVALID_ARG, "%s is NULL", what);
+    for (int i = 0; i < B; ++i) {
+        if (ids[i] < 0 || ids[i] >= s->y.Bmax) return fail(PUZZLEKV_ERR_INVALID_ARG, "%s: slot %d out of range", what, ids[i]);
+        for (int j = 0; j < i; ++j)
+            if (ids[j] == ids[i]) return fail(PUZZLEKV_ERR_INVALID_ARG, "%s: slot %d listed twice", what, ids[i]);
+    }
+    return PUZZLEKV_OK;
+}
+
+// The list of a chunk call: counts >= 0, no sequence past its capacity.
+puzzlekv_status check_chunk(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *counts, int32_t B) {
+    const puzzlekv_status st = check_list(s, seq_ids, B, "seq_ids");
+    if (st != PUZZLEKV_OK) return st;
+    if (layer < 0 || layer >= s->y.L) return fail(PUZZLEKV_ERR_INVALID_ARG, "layer %d out of range", layer);
+    if (!counts) return fail(PUZZLEKV_ERR_INVALID_ARG, "counts is NULL");
+    for (int i = 0; i < B; ++i) {
+        if (counts[i] < 0) return fail(PUZZLEKV_ERR_INVALID_ARG, "counts[%d] is negative", i);
+        const int T = length_of(s, seq_ids[i], layer);
+        if (counts[i] > s->y.Tmax - T)
+            return fail(PUZZLEKV_ERR_CAPACITY, "sequence %d: %d + %d tokens exceed max_tokens_per_seq=%d", seq_ids[i], T,
+                        counts[i], s->y.Tmax);
+    }
+    return PUZZLEKV_OK;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// What a chunk attention call places in its workspace.
+struct AttnPlan {
+    ChunkAttnParams a{};
+    int seq[MAX_CALL_BATCH];
+    long long rows = 0;  // dense key / value rows of the listed sequences
+    size_t v_off = 0, part_off = 0, bytes = 0;
+};
+
+void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *counts, int32_t B,
+                    AttnPlan &pl) {
+    const Layout &y = s->y;
+    ChunkAttnParams &a = pl.a;
+    a.H = y.H; a.Hq = y.Hq; a.G = y.G; a.d = y.d;
+    a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)y.d));
+    long tiles = 0;
+    int off = 0;
+    for (int i = 0; i < B; ++i) {
+        const int n = counts[i], T = length_of(s, seq_ids[i], layer);
+        const int j = a.nseq;
+        if (n > 0) {
+            pl.seq[j] = seq_ids[i];
+            a.T[j] = T;
+            a.n[j] = n;
+            a.off[j] = off;
+            a.koff[j] = pl.rows;
+            pl.rows += T + n;
+            tiles += (long)y.H * ((n * (long)y.G + 31) / 32);
+            ++a.nseq;
+        }
+        off += n;
+    }
+    // few query tiles: cut the keys so that about four CTAs land on every SM
+    const int want = tiles > 0 ? (int)std::max(1L, 4L * s->num_sms / tiles) : 1;
+    long long parts = 0;
+    for (int j = 0; j < a.nseq; ++j) {
+        a.ns[j] = std::max(1, std::min(want, (a.T[j] + a.n[j]) / 64));
+        a.poff[j] = parts;
+        if (a.ns[j] > 1) parts += (long long)y.H * a.ns[j] * a.n[j] * y.G;
+    }
+    const size_t rows_bytes = (size_t)pl.rows * y.H * y.d * y.esz;
+    pl.v_off = up256(rows_bytes);
+    pl.part_off = pl.v_off + up256(rows_bytes);
+    pl.bytes = pl.part_off + up256((size_t)parts * (y.d + 4) * 4);
+}
+
+// Pages of an appended sequence that leave the dense region without factors.
+struct LeavePlan {
+    std::vector<int> pages;
+    bool gather = false;  // some page's rows are not all in the ring once the chunk is in
+};
+
+void plan_leaving(const puzzlekv_store *s, int b, int layer, int n, LeavePlan &lp) {
+    const Layout &y = s->y;
+    const int T0 = length_of(s, b, layer), T1 = T0 + n;
+    lp.pages.clear();
+    lp.gather = false;
+    if (n == 0) return;
+    const int last = (T1 - 1) / y.P;
+    for (int p = std::max(y.sink_pages, (T0 - y.W) / y.P - 1); p <= last; ++p) {
+        if (page_kind(p, T1, y.P, y.sink_tokens, y.W) == KIND_DENSE) continue;
+        if (p * y.P < T0 && page_kind(p, T0, y.P, y.sink_tokens, y.W) == KIND_FACTORED) continue;
+        if (T0 > 0 && has_factors(s, b, layer, p)) continue;
+        lp.pages.push_back(p);
+        if (p <= last - y.ring) lp.gather = true;
+    }
+}
+
+size_t gather_bytes(const Layout &y, const LeavePlan &lp) {
+    if (!lp.gather) return 0;
+    const size_t rows = (size_t)(lp.pages.back() - lp.pages.front() + 1) * y.P;
+    return 2 * up256(rows * y.H * y.d * y.esz);
+}
+
+void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
+    rp = RowsParams{};
+    rp.y = s->y;
+    rp.factor_pool = s->factor_pool;
+    rp.dense_pool = s->dense_pool;
+    rp.rope_base = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_base_offset);
+    rp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_delta_offset);
+    rp.layer = layer;
+    rp.turn = 1;
+}
+
+puzzlekv_status check_work(const void *work, size_t have, size_t need) {
+    if (need == 0) return PUZZLEKV_OK;
+    if (!work || (reinterpret_cast<uintptr_t>(work) & 255u) != 0)
+        return fail(PUZZLEKV_ERR_INVALID_ARG, "the workspace must be non-NULL and 256-byte aligned");
+    if (have < need) return fail(PUZZLEKV_ERR_INVALID_ARG, "the workspace holds %zu bytes, this call needs %zu", have, need);
+    return PUZZLEKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids,
+                                         const int32_t *counts, int32_t B, size_t *attention_bytes,
+                                         size_t *append_bytes) {
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_chunk(s, layer, seq_ids, counts, B);
+        if (st != PUZZLEKV_OK) return st;
+        if (attention_bytes) {
+            AttnPlan pl;
+            plan_attention(s, layer, seq_ids, counts, B, pl);
+            *attention_bytes = pl.a.nseq ? pl.bytes : 0;
+        }
+        if (append_bytes) {
+            *append_bytes = 0;
+            LeavePlan lp;
+            for (int i = 0; i < B; ++i) {
+                plan_leaving(s, seq_ids[i], layer, counts[i], lp);
+                *append_bytes += gather_bytes(s->y, lp);
+            }
+        }
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const void *q, const void *k, const void *v,
+                                         void *out, const int32_t *seq_ids, const int32_t *counts, int32_t B,
+                                         void *work, size_t work_bytes, void *stream) {
+    NvtxRange nvtx_range("puzzlekv_chunk_attention");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_chunk(s, layer, seq_ids, counts, B);
+        if (st != PUZZLEKV_OK) return st;
+        if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "q, k, v and out must be non-NULL and 16-byte aligned");
+        const Layout &y = s->y;
+        AttnPlan pl;
+        plan_attention(s, layer, seq_ids, counts, B, pl);
+        ChunkAttnParams &a = pl.a;
+        if (a.nseq == 0) return PUZZLEKV_OK;
+        st = check_work(work, work_bytes, pl.bytes);
+        if (st != PUZZLEKV_OK) return st;
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        char *w = static_cast<char *>(work);
+        wait_conversions(s, strm, pl.seq, a.T, a.nseq);
+        RowsParams rp;
+        rows_params(s, layer, rp);
+        rp.k_new = static_cast<const char *>(k);
+        rp.v_new = static_cast<const char *>(v);
+        rp.k_out = w;
+        rp.v_out = w + pl.v_off;
+        rp.row_stride = (size_t)y.H * y.d;
+        rp.head_stride = y.d;
+        rp.nseq = a.nseq;
+        for (int j = 0; j < a.nseq; ++j) {
+            rp.seqs[j] = pl.seq[j];
+            rp.T[j] = a.T[j];
+            rp.lo[j] = 0;
+            rp.n[j] = a.T[j] + a.n[j];
+            rp.off[j] = (int)a.koff[j];
+            rp.coff[j] = a.off[j];
+        }
+        a.q = static_cast<const char *>(q);
+        a.out = static_cast<char *>(out);
+        a.K = w;
+        a.V = w + pl.v_off;
+        a.partials = reinterpret_cast<float *>(w + pl.part_off);
+        s->after_decode = false;
+        cudaError_t e = launch_rows(rp, strm);
+        if (e == cudaSuccess) e = launch_chunk_simple(a, y.dtype, strm);
+        if (e == cudaSuccess) e = launch_chunk_merge(a, y.dtype, strm);
+        if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_append_chunk(puzzlekv_store *s, int32_t layer, const void *k, const void *v,
+                                      const int32_t *seq_ids, const int32_t *counts, int32_t B, void *work,
+                                      size_t work_bytes, void *stream) {
+    NvtxRange nvtx_range("puzzlekv_append_chunk");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_chunk(s, layer, seq_ids, counts, B);
+        if (st != PUZZLEKV_OK) return st;
+        if (!k || !v || !aligned16(k) || !aligned16(v))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "k and v must be non-NULL and 16-byte aligned");
+        const Layout &y = s->y;
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        std::vector<LeavePlan> leave(B);
+        AppendChunkParams ap{};
+        ap.y = y;
+        ap.lengths = lengths_ptr(s);
+        ap.desc = desc_ptr(s);
+        ap.dense_pool = s->dense_pool;
+        ap.k = static_cast<const char *>(k);
+        ap.v = static_cast<const char *>(v);
+        ap.layer = layer;
+        ap.nseq = B;
+        size_t need = 0;
+        int grown[MAX_CALL_BATCH], off = 0;
+        for (int i = 0; i < B; ++i) {
+            plan_leaving(s, seq_ids[i], layer, counts[i], leave[i]);
+            need += gather_bytes(y, leave[i]);
+            ap.seqs[i] = seq_ids[i];
+            ap.T[i] = length_of(s, seq_ids[i], layer);
+            ap.n[i] = counts[i];
+            ap.off[i] = off;
+            grown[i] = ap.T[i] + counts[i];
+            off += counts[i];
+        }
+        if (off == 0) return PUZZLEKV_OK;
+        st = check_work(work, work_bytes, need);
+        if (st == PUZZLEKV_OK) st = refuse_capture(strm);
+        if (st != PUZZLEKV_OK) return st;
+        // a page converted in the background becomes factorized, or its ring
+        // slot is written, only past its batch's deadline
+        wait_conversions(s, strm, seq_ids, grown, B);
+        s->after_decode = false;
+        FactorParams fp{};
+        fp.max_ql_iter = 30;
+        fp.status = status_ptr(s);
+        fp.y = y;
+        fp.P = y.P;
+        fp.d = y.d;
+        fp.x_esz = y.esz;
+        fp.factor_pool = s->factor_pool;
+        cudaError_t e = cudaSuccess;
+        // pages whose rows the ring will not hold: from a copy of their rows
+        // (old rows of the ring, then the chunk's) made before the ring changes
+        size_t at = 0;
+        for (int i = 0; i < B && e == cudaSuccess; ++i) {
+            const LeavePlan &lp = leave[i];
+            if (!lp.gather) continue;
+            const int lo = lp.pages.front(), rows = (lp.pages.back() - lo + 1) * y.P;
+            const size_t half = gather_bytes(y, lp) / 2;
+            RowsParams rp;
+            rows_params(s, layer, rp);
+            rp.turn = 0;
+            rp.k_new = ap.k;
+            rp.v_new = ap.v;
+            rp.k_out = static_cast<char *>(work) + at;
+            rp.v_out = rp.k_out + half;
+            rp.row_stride = y.d;
+            rp.head_stride = (size_t)rows * y.d;
+            rp.nseq = 1;
+            rp.seqs[0] = seq_ids[i];
+            rp.T[0] = ap.T[i];
+            rp.lo[0] = lo * y.P;
+            rp.n[0] = rows;
+            rp.coff[0] = ap.off[i];
+            e = launch_rows(rp, strm);
+            fp.mode = FACT_MODE_PREFILL;
+            const size_t shift = (size_t)lo * y.P * y.d * y.esz;  // page lo is the copy's first
+            fp.k_src = rp.k_out - shift;
+            fp.v_src = rp.v_out - shift;
+            fp.seq = seq_ids[i];
+            fp.T = rows;
+            fp.layer0 = layer;
+            fp.n_layers = 1;
+            for (size_t a = 0; a < lp.pages.size() && e == cudaSuccess;) {  // runs of consecutive pages
+                size_t z = a + 1;
+                while (z < lp.pages.size() && lp.pages[z] == lp.pages[z - 1] + 1) ++z;
+                fp.p_lo = lp.pages[a];
+                fp.p_hi = lp.pages[z - 1] + 1;
+                fp.n_jobs = (long)y.H * 2 * (fp.p_hi - fp.p_lo);
+                e = launch_factorize(fp, s->num_sms, strm);
+                a = z;
+            }
+            at += 2 * half;
+        }
+        if (e == cudaSuccess) e = launch_append_chunk(ap, strm);
+        // the other leaving pages are whole in the ring
+        fp.mode = FACT_MODE_CONVERT;
+        fp.dense_pool = s->dense_pool;
+        fp.layer = layer;
+        fp.n_conv = 0;
+        auto flush = [&]() {
+            if (fp.n_conv == 0 || e != cudaSuccess) return;
+            fp.n_jobs = (long)fp.n_conv * y.H * 2;
+            e = launch_factorize(fp, s->num_sms, strm);
+            fp.n_conv = 0;
+        };
+        for (int i = 0; i < B; ++i) {
+            if (leave[i].gather) continue;
+            for (int p : leave[i].pages) {
+                if (fp.n_conv == MAX_CALL_BATCH) flush();
+                fp.conv_seq[fp.n_conv] = seq_ids[i];
+                fp.conv_page[fp.n_conv++] = p;
+            }
+        }
+        flush();
+        if (e != cudaSuccess) return cuda_fail(e, "chunk append launch");
+        for (int i = 0; i < B; ++i) {
+            if (counts[i] == 0) continue;
+            const int b = seq_ids[i];
+            if (ap.T[i] == 0) {
+                reset_factors(s, b, layer, y.sink_pages);
+                s->dense_lo[(size_t)b * y.L + layer] = y.sink_pages;
+            }
+            for (int p : leave[i].pages) set_factors(s, b, layer, p);
+            grow_dense(s, b, layer, s->len[(size_t)b * y.L + layer] = grown[i]);
+        }
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *starts,
+                                     const int32_t *counts, int32_t B, void *k, void *v, void *stream) {
+    NvtxRange nvtx_range("puzzlekv_read_tokens");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_list(s, seq_ids, B, "seq_ids");
+        if (st != PUZZLEKV_OK) return st;
+        const Layout &y = s->y;
+        if (layer < 0 || layer >= y.L) return fail(PUZZLEKV_ERR_INVALID_ARG, "layer %d out of range", layer);
+        if (!starts || !counts) return fail(PUZZLEKV_ERR_INVALID_ARG, "starts and counts must be non-NULL");
+        if (!k || !v || !aligned16(k) || !aligned16(v))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "k and v must be non-NULL and 16-byte aligned");
+        RowsParams rp;
+        rows_params(s, layer, rp);
+        int lens[MAX_CALL_BATCH], off = 0;
+        for (int i = 0; i < B; ++i) {
+            const int T = length_of(s, seq_ids[i], layer);
+            if (starts[i] < 0 || counts[i] < 0 || starts[i] > T || counts[i] > T - starts[i])
+                return fail(PUZZLEKV_ERR_INVALID_ARG, "entry %d: rows [%d, %d + %d) of a sequence of %d tokens", i, starts[i],
+                            starts[i], counts[i], T);
+            rp.seqs[i] = seq_ids[i];
+            lens[i] = rp.T[i] = T;
+            rp.lo[i] = starts[i];
+            rp.n[i] = counts[i];
+            rp.off[i] = off;
+            off += counts[i];
+        }
+        if (off == 0) return PUZZLEKV_OK;
+        rp.nseq = B;
+        rp.k_out = static_cast<char *>(k);
+        rp.v_out = static_cast<char *>(v);
+        rp.row_stride = (size_t)y.H * y.d;
+        rp.head_stride = y.d;
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        wait_conversions(s, strm, seq_ids, lens, B);
+        s->after_decode = false;
+        const cudaError_t e = launch_rows(rp, strm);
+        if (e != cudaSuccess) return cuda_fail(e, "row read launch");
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_load_factors(puzzlekv_store *s, int32_t layer, int32_t seq, int32_t page0, int32_t n,
+                                      const void *LK, const void *RK, const void *LV, const void *RV, void *stream) {
+    NvtxRange nvtx_range("puzzlekv_load_factors");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_list(s, &seq, 1, "seq");
+        if (st != PUZZLEKV_OK) return st;
+        const Layout &y = s->y;
+        if (layer < 0 || layer >= y.L) return fail(PUZZLEKV_ERR_INVALID_ARG, "layer %d out of range", layer);
+        if (y.q4) return fail(PUZZLEKV_ERR_UNSUPPORTED, "INT4 records take no plain factors");
+        const int complete = length_of(s, seq, layer) / y.P;
+        if (n < 0 || page0 < y.sink_pages || page0 > complete || n > complete - page0)
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "pages [%d, %d + %d): sequence %d has complete pages [%d, %d) past its sink",
+                        page0, page0, n, seq, y.sink_pages, complete);
+        if (n == 0) return PUZZLEKV_OK;
+        if (!LK || !RK || !LV || !RV) return fail(PUZZLEKV_ERR_INVALID_ARG, "factors must be non-NULL");
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        st = refuse_capture(strm);
+        if (st != PUZZLEKV_OK) return st;
+        wait_conversions(s, strm, nullptr, nullptr, 0, true);  // a pending batch may hold one of the pages
+        s->after_decode = false;
+        LoadFactorsParams p{};
+        p.y = y;
+        p.factor_pool = s->factor_pool;
+        p.LK = static_cast<const char *>(LK);
+        p.RK = static_cast<const char *>(RK);
+        p.LV = static_cast<const char *>(LV);
+        p.RV = static_cast<const char *>(RV);
+        p.layer = layer;
+        p.seq = seq;
+        p.page0 = page0;
+        p.n = n;
+        const cudaError_t e = launch_load_factors(p, strm);
+        if (e != cudaSuccess) return cuda_fail(e, "factor load launch");
+        for (int g = page0; g < page0 + n; ++g) set_factors(s, seq, layer, g);
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_copy_sequences(puzzlekv_store *s, const int32_t *src_ids, const int32_t *dst_ids, int32_t n,
+                                        void *stream) {
+    NvtxRange nvtx_range("puzzlekv_copy_sequences");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_list(s, dst_ids, n, "dst_ids");
+        if (st != PUZZLEKV_OK) return st;
+        if (!src_ids) return fail(PUZZLEKV_ERR_INVALID_ARG, "src_ids is NULL");
+        const Layout &y = s->y;
+        CopyParams p{};
+        p.y = y;
+        p.factor_pool = s->factor_pool;
+        p.dense_pool = s->dense_pool;
+        p.lengths = lengths_ptr(s);
+        p.desc = desc_ptr(s);
+        p.status = status_ptr(s);
+        for (int i = 0; i < n; ++i) {
+            const int b = src_ids[i];
+            if (b < 0 || b >= y.Bmax) return fail(PUZZLEKV_ERR_INVALID_ARG, "src_ids: slot %d out of range", b);
+            const int T = length_of(s, b, 0);
+            if (T < 1) return fail(PUZZLEKV_ERR_INVALID_ARG, "src_ids: sequence %d holds no tokens", b);
+            for (int l = 1; l < y.L; ++l)
+                if (length_of(s, b, l) != T)
+                    return fail(PUZZLEKV_ERR_INVALID_ARG, "src_ids: sequence %d has layers of different lengths", b);
+            if (b == dst_ids[i]) continue;
+            int j = 0;
+            while (j < p.nsrc && p.src[j] != b) ++j;
+            if (j == p.nsrc) {
+                p.src[j] = b;
+                p.T[j] = T;
+                const int pages = (T + y.P - 1) / y.P;
+                int lo = pages;  // first page past the sink that some layer still holds densely
+                for (int l = 0; l < y.L; ++l) {
+                    const size_t x = (size_t)b * y.L + l;
+                    int upto = s->conv_upto[x];
+                    for (int g = (int)s->marked[x].size() - 1; g >= upto; --g)
+                        if (s->marked[x][g]) {
+                            upto = g + 1;
+                            break;
+                        }
+                    p.upto[j] = std::max(p.upto[j], upto);
+                    lo = std::min(lo, std::max(s->dense_lo[x], y.sink_pages));
+                }
+                for (int g = 0; g < std::min(y.sink_pages, pages); ++g) p.slots[j] |= 1ull << y.dense_slot(g);
+                for (int g = lo; g < pages; ++g) p.slots[j] |= 1ull << y.dense_slot(g);
+                ++p.nsrc;
+            }
+            p.dst[p.npair] = dst_ids[i];
+            p.pair_src[p.npair] = j;
+            for (int l = 0; l < y.L; ++l)
+                p.had[p.npair] = std::max(p.had[p.npair], (length_of(s, dst_ids[i], l) + y.P - 1) / y.P);
+            ++p.npair;
+        }
+        if (p.npair == 0) return PUZZLEKV_OK;
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        st = refuse_capture(strm);
+        if (st != PUZZLEKV_OK) return st;
+        // the sources' bookkeeping before any destination's changes
+        std::vector<int> len, upto, lo;
+        std::vector<std::vector<uint8_t>> marked;
+        for (int j = 0; j < p.nsrc; ++j)
+            for (int l = 0; l < y.L; ++l) {
+                const size_t x = (size_t)p.src[j] * y.L + l;
+                len.push_back(s->len[x]);
+                upto.push_back(s->conv_upto[x]);
+                lo.push_back(s->dense_lo[x]);
+                marked.push_back(s->marked[x]);
+            }
+        wait_conversions(s, strm, nullptr, nullptr, 0, true);
+        s->after_decode = false;
+        const cudaError_t e = launch_copy(p, s->num_sms, strm);
+        if (e != cudaSuccess) return cuda_fail(e, "sequence copy launch");
+        for (int i = 0; i < p.npair; ++i)
+            for (int l = 0; l < y.L; ++l) {
+                const size_t x = (size_t)p.dst[i] * y.L + l, z = (size_t)p.pair_src[i] * y.L + l;
+                s->len[x] = len[z];
+                s->conv_upto[x] = upto[z];
+                s->dense_lo[x] = lo[z];
+                s->marked[x] = marked[z];
+            }
+        return PUZZLEKV_OK;
+    });
+}
+
+puzzlekv_status puzzlekv_truncate_sequences(puzzlekv_store *s, const int32_t *seq_ids, const int32_t *lengths, int32_t B,
+                                            void *stream) {
+    NvtxRange nvtx_range("puzzlekv_truncate_sequences");
+    return guarded([&]() -> puzzlekv_status {
+        puzzlekv_status st = check_list(s, seq_ids, B, "seq_ids");
+        if (st != PUZZLEKV_OK) return st;
+        if (!lengths) return fail(PUZZLEKV_ERR_INVALID_ARG, "lengths is NULL");
+        const Layout &y = s->y;
+        TruncateParams p{};
+        p.y = y;
+        p.lengths = lengths_ptr(s);
+        p.desc = desc_ptr(s);
+        p.nseq = B;
+        for (int i = 0; i < B; ++i) {
+            const int b = seq_ids[i], T = lengths[i];
+            if (T < 0) return fail(PUZZLEKV_ERR_INVALID_ARG, "lengths[%d] is negative", i);
+            const int pages = (T + y.P - 1) / y.P;
+            int fw = pages;  // first dense page of the shorter sequence past its sink
+            while (fw > y.sink_pages && page_kind(fw - 1, T, y.P, y.sink_tokens, y.W) == KIND_DENSE) --fw;
+            for (int l = 0; l < y.L; ++l) {
+                const int have = length_of(s, b, l);
+                if (T > have)
+                    return fail(PUZZLEKV_ERR_INVALID_ARG, "sequence %d holds %d tokens in layer %d, fewer than %d", b, have, l, T);
+                if (T < have && fw < pages && fw >= y.sink_pages && fw < s->dense_lo[(size_t)b * y.L + l])
+                    return fail(PUZZLEKV_ERR_INVALID_ARG,
+                                "sequence %d cannot go back to %d tokens: page %d would be dense and its rows are gone "
+                                "(kept from page %d on)", b, T, fw, s->dense_lo[(size_t)b * y.L + l]);
+                p.had[i] = std::max(p.had[i], (have + y.P - 1) / y.P);
+            }
+            p.seqs[i] = b;
+            p.T[i] = T;
+        }
+        cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        st = refuse_capture(strm);
+        if (st != PUZZLEKV_OK) return st;
+        wait_conversions(s, strm, nullptr, nullptr, 0, true);  // a pending batch may hold a page that is cut off
+        s->after_decode = false;
+        const cudaError_t e = launch_truncate(p, strm);
+        if (e != cudaSuccess) return cuda_fail(e, "truncate launch");
+        for (int i = 0; i < B; ++i)
+            for (int l = 0; l < y.L; ++l) {
+                const size_t x = (size_t)p.seqs[i] * y.L + l;
+                const int T = p.T[i], complete = T / y.P;
+                s->len[x] = T > 0 ? T : -1;
+                if (T == 0) {
+                    reset_factors(s, p.seqs[i], l, y.sink_pages);
+                    s->dense_lo[x] = y.sink_pages;
+                    continue;
+                }
+                // a page cut into is filled again with other tokens: its factors are void
+                s->conv_upto[x] = std::max(y.sink_pages, std::min(s->conv_upto[x], complete));
+                std::vector<uint8_t> &m = s->marked[x];
+                for (size_t g = complete; g < m.size(); ++g) m[g] = 0;
+            }
+        return PUZZLEKV_OK;
+    });
+}
+
+}  // extern "C"

@@ -102,6 +102,102 @@ struct AppendParams {
     int conv_page[MAX_CALL_BATCH]; // page converted by this call, or -1
 };
 
+// Rows of the cache of a list of sequences, as attention sees them: row t of
+// call entry i comes from the store for t < T[i] (factorized pages rebuilt as
+// L R, keys stored before RoPE turned when `turn` is set) and from the chunk
+// k_new / v_new ([sum n][H][d], entry i's tokens from row coff[i] on) beyond.
+// Rows lo[i] .. lo[i] + n[i] - 1 go to k_out / v_out: row r of the call's rows
+// (entry i's from off[i] on) at element r * row_stride + head * head_stride.
+struct RowsParams {
+    Layout y;
+    const char *factor_pool, *dense_pool;
+    const float2 *rope_base, *rope_delta;
+    const char *k_new, *v_new;
+    char *k_out, *v_out;
+    size_t row_stride, head_stride;  // elements
+    int layer, nseq, turn;
+    int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], lo[MAX_CALL_BATCH], n[MAX_CALL_BATCH];
+    int off[MAX_CALL_BATCH], coff[MAX_CALL_BATCH];
+    int page_off[MAX_CALL_BATCH + 1];  // pages touched by the entries before (filled by the launcher)
+};
+
+// Chunk append: rows T[i] .. T[i] + n[i] - 1 of entry i, from k / v ([sum
+// n][H][d], entry i's from off[i] on), into the dense pages still in the
+// sink or the ring at length T[i] + n[i]; lengths and page kinds follow.
+struct AppendChunkParams {
+    Layout y;
+    int *lengths, *desc;
+    char *dense_pool;
+    const char *k, *v;
+    int layer, nseq;
+    int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH];
+};
+
+// Lengths and page kinds of the listed sequences at a new (shorter) length T[i]
+// in every layer; had[i] is the number of pages described before.
+struct TruncateParams {
+    Layout y;
+    int *lengths, *desc;
+    int nseq;
+    int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], had[MAX_CALL_BATCH];
+};
+
+// Plain factors of n pages from page0 on into their records: LK [H][n][P][rk],
+// RK [H][n][rk][d], LV [H][n][P][rv], RV [H][n][rv][d], storage dtype.
+struct LoadFactorsParams {
+    Layout y;
+    char *factor_pool;
+    const char *LK, *RK, *LV, *RV;
+    int layer, seq, page0, n;
+};
+
+// Every listed destination slot takes its source's pages, as if all were
+// copied at once: src[j] are the distinct sources; pair i copies source
+// pair_src[i] (an index into src) to slot dst[i].
+struct CopyParams {
+    Layout y;
+    char *factor_pool, *dense_pool;
+    int *lengths, *desc;
+    int *status;
+    int nsrc, npair;
+    int src[MAX_CALL_BATCH], T[MAX_CALL_BATCH];          // per source: slot, length
+    int upto[MAX_CALL_BATCH];                            // page after its last factor record
+    unsigned long long slots[MAX_CALL_BATCH];            // its dense slots in use
+    int dst[MAX_CALL_BATCH], pair_src[MAX_CALL_BATCH];
+    int had[MAX_CALL_BATCH];                             // pages the destination's table described
+    // filled by the launcher
+    int max_upto, tile;
+    unsigned long long any_slots;
+};
+
+// Attention of a chunk of queries over rows laid out densely, and the merge
+// of split states.  Entry i holds n[i] tokens (rows off[i] .. of q and out,
+// [sum n][Hq][d]); its T[i] + n[i] key / value rows start at row koff[i] of K /
+// V ([rows][H][d]); query token j sees the first T[i] + j + 1.  Row r of the
+// n G query rows of (entry, KV head) is token r / G, head r % G.  With ns[i] >
+// 1 the keys are cut into ns[i] ranges whose states (m in log2 units, l, two
+// pad floats, o[d]) go to row poff[i] + (head ns[i] + split) n[i] G + r of
+// `partials`.
+struct ChunkAttnParams {
+    int H, Hq, G, d, nseq;
+    float scale_log2;  // log2(e) / sqrt(d)
+    const char *q;
+    const char *K, *V;
+    char *out;
+    float *partials;
+    int T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH], ns[MAX_CALL_BATCH];
+    long long koff[MAX_CALL_BATCH], poff[MAX_CALL_BATCH];
+    int tile_off[MAX_CALL_BATCH + 1];  // CTAs of the entries before (filled by the launcher)
+};
+
+cudaError_t launch_rows(RowsParams &p, cudaStream_t st);
+cudaError_t launch_append_chunk(const AppendChunkParams &p, cudaStream_t st);
+cudaError_t launch_truncate(const TruncateParams &p, cudaStream_t st);
+cudaError_t launch_load_factors(const LoadFactorsParams &p, cudaStream_t st);
+cudaError_t launch_copy(CopyParams &p, int num_sms, cudaStream_t st);
+cudaError_t launch_chunk_simple(ChunkAttnParams &p, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_merge(const ChunkAttnParams &p, int dtype, cudaStream_t st);
+
 cudaError_t launch_factorize(const FactorParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_seq_init(const SeqInitParams &p, cudaStream_t st);
 cudaError_t launch_append(const AppendParams &p, cudaStream_t st);

@@ -1,0 +1,241 @@
+// Rows in and out of the paged cache: reading rows as attention sees them,
+// appending a chunk of tokens, and placing plain factors in a store's records
+// ("PuzzleKV: Page-Wise Low-Rank Decomposition for KV Cache Compression",
+// §3.3 ③-⑤).  Page kinds follow page_kind() in layout.h.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace pkv {
+
+// Dequantize one factor of an INT4 record (K x N operand starting at register
+// m0 of the stream) to fp32 at put(k, n, code).
+template <typename F>
+__device__ __forceinline__ void q4_codes(const char *stream, int m0, int K, int N, F put) {
+    const int regs = q4_operand_regs(K, N);
+    for (int i = threadIdx.x; i < regs * 32; i += blockDim.x) {
+        const int m = m0 + i / 32, lane = i % 32, w = m / 4;
+        const uint32_t word = *reinterpret_cast<const uint32_t *>(stream + ((w / 2) * 32 + lane) * 8 + (w % 2) * 4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            int k, n;
+            q4_operand_elem(K, N, m - m0, lane, e, k, n);
+            put(k, n, (float)((int)((word >> (4 * ((m % 4) + 4 * e))) & 15u) - 8));
+        }
+    }
+}
+
+// A page's factors in fp32: L [P][rp] at `Ls`, R [rp][d] at `Rs` (shared memory).
+template <typename T>
+__device__ void load_page_factors(const Layout &y, const char *rec, int kv, float *Ls, float *Rs) {
+    const int P = y.P, d = y.d, rp = kv == 0 ? y.rkp : y.rvp;
+    if (y.q4) {
+        auto sc = [&](size_t off, int i) {
+            return __half2float(reinterpret_cast<const __half *>(rec + off)[i]);
+        };
+        if (kv == 0) {
+            q4_codes(rec, 0, d, rp, [&](int k, int n, float c) { Rs[n * d + k] = c * sc(y.q_off_sRK, q4_dscale_index(k)); });
+            q4_codes(rec, q4_operand_regs(d, rp), rp, P,
+                     [&](int k, int n, float c) { Ls[n * rp + k] = c * sc(y.q_off_sLK, q4_scale_index(rp, k)); });
+        } else {
+            const char *vs = rec + y.q_off_V;
+            q4_codes(vs, 0, P, rp, [&](int k, int n, float c) { Ls[k * rp + n] = c * sc(y.q_off_sLV, q4_scale_index(P, k)); });
+            q4_codes(vs, q4_operand_regs(P, rp), rp, d,
+                     [&](int k, int n, float c) { Rs[k * d + n] = c * sc(y.q_off_sRV, q4_dscale_index(n)); });
+        }
+        return;
+    }
+    if (kv == 0) {
+        for (int e = threadIdx.x; e < P * rp; e += blockDim.x) Ls[e] = Elem<T>::load(swz_ptr<T>(rec, e / rp, e % rp, rp));
+        for (int e = threadIdx.x; e < rp * d; e += blockDim.x)
+            Rs[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_RK, e / d, e % d, d));
+    } else {
+        for (int e = threadIdx.x; e < P * rp; e += blockDim.x)
+            Ls[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_LV, e % rp, e / rp, P));
+        for (int e = threadIdx.x; e < rp * d; e += blockDim.x)
+            Rs[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_RV, e % d, e / d, rp));
+    }
+}
+
+// Block (page of a call entry, head, K/V): the page's rows inside the entry's
+// range.  Each thread holds columns c and c + d/2 of its rows, the pair that
+// RoPE turns together.
+template <typename T>
+__global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
+    extern __shared__ __align__(16) float sm[];
+    const Layout &y = p.y;
+    const int P = y.P, d = y.d, h = blockIdx.y, kv = blockIdx.z;
+    int i = 0;
+    while ((int)blockIdx.x >= p.page_off[i + 1]) ++i;
+    const int lo = p.lo[i], hi = lo + p.n[i], T0 = p.T[i], b = p.seqs[i];
+    const int pg = lo / P + (int)blockIdx.x - p.page_off[i];
+    const int r0 = max(lo, pg * P), r1 = min(hi, pg * P + P);
+    const bool cached = pg * P < T0;
+    const bool factored = cached && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
+    const int rp = kv == 0 ? y.rkp : y.rvp;
+    float *Ls = sm, *Rs = sm + P * rp;
+    const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, kv);
+    if (factored) {
+        load_page_factors<T>(y, p.factor_pool + y.record_offset(p.layer, b, h, pg), kv, Ls, Rs);
+        __syncthreads();
+    }
+    const T *chunk = reinterpret_cast<const T *>(kv == 0 ? p.k_new : p.v_new);
+    T *out = reinterpret_cast<T *>(kv == 0 ? p.k_out : p.v_out);
+    const int half = d / 2, c = threadIdx.x % half, step = blockDim.x / half;
+    const bool turn = kv == 0 && y.rope && p.turn;
+    for (int r = r0 + threadIdx.x / half; r < r1; r += step) {
+        const int t = r - pg * P;
+        T x0, x1;
+        float f0 = 0.f, f1 = 0.f;
+        if (factored) {
+            for (int j = 0; j < rp; ++j) {
+                const float l = Ls[t * rp + j];
+                f0 = fmaf(l, Rs[j * d + c], f0);
+                f1 = fmaf(l, Rs[j * d + c + half], f1);
+            }
+        } else {
+            if (r < T0) {
+                x0 = *swz_ptr<T>(page, t, c, d);
+                x1 = *swz_ptr<T>(page, t, c + half, d);
+            } else {
+                const T *src = chunk + ((size_t)(p.coff[i] + r - T0) * y.H + h) * d;
+                x0 = src[c];
+                x1 = src[c + half];
+            }
+            f0 = Elem<T>::load(&x0);
+            f1 = Elem<T>::load(&x1);
+        }
+        if (turn) {  // position pg P + t: the page start's angle plus the offset's
+            const float2 a = p.rope_base[(size_t)pg * half + c], o = p.rope_delta[t * half + c];
+            const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
+            const float u0 = f0 * cs - f1 * sn, u1 = f1 * cs + f0 * sn;
+            f0 = u0;
+            f1 = u1;
+        }
+        if (factored || turn) {
+            x0 = Elem<T>::from_f32(f0);
+            x1 = Elem<T>::from_f32(f1);
+        }
+        T *dst = out + (size_t)(p.off[i] + r - lo) * p.row_stride + (size_t)h * p.head_stride;
+        dst[c] = x0;
+        dst[c + half] = x1;
+    }
+}
+
+// Block (group of 16 rows, head, call entry): rows that stay in a dense page.
+// A row of the chunk whose page has already left the ring at the new length is
+// not written (its page is factorized from the caller's rows).  Block (0, 0,
+// entry) also writes the entry's length and the page kinds from its first page
+// that was dense on.
+template <typename T>
+__global__ void append_chunk_kernel(const AppendChunkParams p) {
+    const Layout &y = p.y;
+    const int i = blockIdx.z, h = blockIdx.y, b = p.seqs[i];
+    const int T0 = p.T[i], T1 = T0 + p.n[i];
+    if (T1 == T0) return;
+    const int last = (T1 - 1) / y.P;
+    if (h == 0 && blockIdx.x == 0) {
+        if (threadIdx.x == 0) p.lengths[y.len_index(b, p.layer)] = T1;
+        const int first = max(0, (T0 - y.W) / y.P - 1);
+        for (int pg = first + threadIdx.x; pg <= last; pg += blockDim.x)
+            p.desc[y.desc_index(b, p.layer, pg)] =
+                page_kind(pg, T1, y.P, y.sink_tokens, y.W) == KIND_DENSE ? (KIND_DENSE << KIND_SHIFT) | y.dense_slot(pg) : pg;
+    }
+    const T *src[2] = {reinterpret_cast<const T *>(p.k), reinterpret_cast<const T *>(p.v)};
+    constexpr int VE = 16 / sizeof(T);  // elements of a 16-byte chunk
+    const int nv = y.d / VE, per_row = 2 * nv;
+    const int j0 = blockIdx.x * 16, j1 = min(p.n[i], j0 + 16);
+    for (int e = threadIdx.x; e < (j1 - j0) * per_row; e += blockDim.x) {
+        const int j = j0 + e / per_row, kv = (e % per_row) / nv, c = e % nv;
+        const int pg = (T0 + j) / y.P, row = (T0 + j) % y.P;
+        if (pg >= y.sink_pages && pg <= last - y.ring) continue;
+        char *dst = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, kv);
+        *reinterpret_cast<uint4 *>(swz_ptr<T>(dst, row, c * VE, y.d)) =
+            reinterpret_cast<const uint4 *>(src[kv] + ((size_t)(p.off[i] + j) * y.H + h) * y.d)[c];
+    }
+}
+
+// Block (call entry, layer): the length, and the kinds of the pages the old
+// length described (pages past the new length become 0).
+__global__ void truncate_kernel(const TruncateParams p) {
+    const Layout &y = p.y;
+    const int i = blockIdx.x, layer = blockIdx.y, b = p.seqs[i], T = p.T[i];
+    if (threadIdx.x == 0) p.lengths[y.len_index(b, layer)] = T;
+    const int n = (T + y.P - 1) / y.P;
+    for (int pg = max(0, (T - y.W) / y.P - 1) + threadIdx.x; pg < p.had[i]; pg += blockDim.x) {
+        int v = 0;
+        if (pg < n)
+            v = page_kind(pg, T, y.P, y.sink_tokens, y.W) == KIND_DENSE ? (KIND_DENSE << KIND_SHIFT) | y.dense_slot(pg) : pg;
+        p.desc[y.desc_index(b, layer, pg)] = v;
+    }
+}
+
+// Block (page, head): the four factors into the record, ranks padded with zeros.
+template <typename T>
+__global__ void load_factors_kernel(const LoadFactorsParams p) {
+    const Layout &y = p.y;
+    const int P = y.P, d = y.d, h = blockIdx.y;
+    char *rec = p.factor_pool + y.record_offset(p.layer, p.seq, h, p.page0 + blockIdx.x);
+    const size_t pg = (size_t)h * p.n + blockIdx.x;
+    const T *LK = reinterpret_cast<const T *>(p.LK) + pg * P * y.rk, *RK = reinterpret_cast<const T *>(p.RK) + pg * y.rk * d;
+    const T *LV = reinterpret_cast<const T *>(p.LV) + pg * P * y.rv, *RV = reinterpret_cast<const T *>(p.RV) + pg * y.rv * d;
+    const T zero = Elem<T>::from_f32(0.f);
+    for (int e = threadIdx.x; e < P * y.rkp; e += blockDim.x) {
+        const int t = e / y.rkp, j = e % y.rkp;
+        *swz_ptr<T>(rec, t, j, y.rkp) = j < y.rk ? LK[t * y.rk + j] : zero;
+    }
+    for (int e = threadIdx.x; e < y.rkp * d; e += blockDim.x) {
+        const int j = e / d, c = e % d;
+        *swz_ptr<T>(rec + y.off_RK, j, c, d) = j < y.rk ? RK[j * d + c] : zero;
+    }
+    for (int e = threadIdx.x; e < y.rvp * P; e += blockDim.x) {
+        const int j = e / P, t = e % P;
+        *swz_ptr<T>(rec + y.off_LV, j, t, P) = j < y.rv ? LV[t * y.rv + j] : zero;
+    }
+    for (int e = threadIdx.x; e < d * y.rvp; e += blockDim.x) {
+        const int c = e / y.rvp, j = e % y.rvp;
+        *swz_ptr<T>(rec + y.off_RV, c, j, y.rvp) = j < y.rv ? RV[j * d + c] : zero;
+    }
+}
+
+cudaError_t launch_rows(RowsParams &p, cudaStream_t st) {
+    const Layout &y = p.y;
+    p.page_off[0] = 0;
+    for (int i = 0; i < p.nseq; ++i)
+        p.page_off[i + 1] = p.page_off[i] + (p.n[i] > 0 ? (p.lo[i] + p.n[i] - 1) / y.P - p.lo[i] / y.P + 1 : 0);
+    if (p.page_off[p.nseq] == 0) return cudaSuccess;
+    const size_t smem = (size_t)(y.P + y.d) * (y.rkp > y.rvp ? y.rkp : y.rvp) * 4;  // at most 48 KB
+    const dim3 grid((unsigned)p.page_off[p.nseq], (unsigned)y.H, 2);
+    if (y.dtype == 1)
+        rows_kernel<__nv_bfloat16><<<grid, 256, smem, st>>>(p);
+    else
+        rows_kernel<float><<<grid, 256, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_append_chunk(const AppendChunkParams &p, cudaStream_t st) {
+    int most = 0;
+    for (int i = 0; i < p.nseq; ++i) most = p.n[i] > most ? p.n[i] : most;
+    if (most == 0) return cudaSuccess;
+    const dim3 grid((unsigned)((most + 15) / 16), (unsigned)p.y.H, (unsigned)p.nseq);
+    if (p.y.dtype == 1)
+        append_chunk_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+    else
+        append_chunk_kernel<float><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_truncate(const TruncateParams &p, cudaStream_t st) {
+    truncate_kernel<<<dim3((unsigned)p.nseq, (unsigned)p.y.L), 128, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_load_factors(const LoadFactorsParams &p, cudaStream_t st) {
+    const dim3 grid((unsigned)p.n, (unsigned)p.y.H);
+    if (p.y.dtype == 1)
+        load_factors_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+    else
+        load_factors_kernel<float><<<grid, 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pkv
