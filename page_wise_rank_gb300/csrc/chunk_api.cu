@@ -77,11 +77,38 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // What a chunk attention call places in its workspace.
 struct AttnPlan {
-    ChunkAttnParams a{};
+    ChunkAttnParams a{};  // fp32 and INT4 stores
+    FlashParams f{};      // other bf16 stores
+    bool flash = false;
     int seq[MAX_CALL_BATCH];
     long long rows = 0;  // dense key / value rows of the listed sequences
-    size_t v_off = 0, part_off = 0, bytes = 0;
+    size_t v_off = 0, scale_off = 0, part_off = 0, bytes = 0;
 };
+
+// The tensor-core path: operand images, their scales, the cut pairs' states.
+void plan_flash(const puzzlekv_store *s, AttnPlan &pl) {
+    const Layout &y = s->y;
+    const ChunkAttnParams &a = pl.a;
+    FlashParams &f = pl.f;
+    f.H = a.H; f.Hq = a.Hq; f.G = a.G;
+    f.scale_log2 = a.scale_log2;
+    f.nseq = a.nseq;
+    for (int j = 0; j < a.nseq; ++j) {
+        f.T[j] = a.T[j];
+        f.n[j] = a.n[j];
+        f.off[j] = a.off[j];
+        f.blk_off[j + 1] = f.blk_off[j] + (a.T[j] + a.n[j] + FLASH_KEYS - 1) / FLASH_KEYS;
+        long long u = 0;
+        for (int p = 0; (long long)p * FLASH_ROWS < (long long)a.n[j] * a.G; ++p) u += flash_blocks(a.T[j], a.n[j], a.G, p);
+        f.head_units[j] = u;
+        f.unit_off[j + 1] = f.unit_off[j] + u * a.H;
+    }
+    f.ctas = (int)std::min<long long>(s->num_sms, std::max(1LL, f.unit_off[f.nseq]));
+    const size_t blocks = (size_t)f.blk_off[f.nseq] * y.H;
+    pl.scale_off = blocks * (2 * FLASH_KEYS * y.d * 2);
+    pl.part_off = pl.scale_off + up256(blocks * sizeof(float2));
+    pl.bytes = pl.part_off + (f.ctas > 1 ? (size_t)2 * f.ctas * FLASH_ROWS * (y.d + 4) * 4 : 0);
+}
 
 void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *counts, int32_t B,
                     AttnPlan &pl) {
@@ -105,6 +132,11 @@ void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_i
             ++a.nseq;
         }
         off += n;
+    }
+    if (y.dtype == 1 && !y.q4) {
+        pl.flash = true;
+        plan_flash(s, pl);
+        return;
     }
     // few query tiles: cut the keys so that about four CTAs land on every SM
     const int want = tiles > 0 ? (int)std::max(1L, 4L * s->num_sms / tiles) : 1;
@@ -213,6 +245,40 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
         char *w = static_cast<char *>(work);
         wait_conversions(s, strm, pl.seq, a.T, a.nseq);
+        if (pl.flash) {
+            StageParams sp{};
+            sp.y = y;
+            sp.factor_pool = s->factor_pool;
+            sp.dense_pool = s->dense_pool;
+            sp.rope_base = reinterpret_cast<const float2 *>(s->workspace + y.rope_base_offset);
+            sp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + y.rope_delta_offset);
+            sp.k_new = static_cast<const char *>(k);
+            sp.v_new = static_cast<const char *>(v);
+            sp.images = w;
+            sp.scales = reinterpret_cast<float2 *>(w + pl.scale_off);
+            sp.status = status_ptr(s);
+            sp.layer = layer;
+            sp.nseq = a.nseq;
+            for (int j = 0; j < a.nseq; ++j) {
+                sp.seqs[j] = pl.seq[j];
+                sp.T[j] = a.T[j];
+                sp.n[j] = a.n[j];
+                sp.off[j] = a.off[j];
+                sp.blk_off[j + 1] = pl.f.blk_off[j + 1];
+            }
+            FlashParams &f = pl.f;
+            f.q = static_cast<const char *>(q);
+            f.out = static_cast<char *>(out);
+            f.images = w;
+            f.scales = sp.scales;
+            f.partials = reinterpret_cast<float *>(w + pl.part_off);
+            f.status = status_ptr(s);
+            s->after_decode = false;
+            cudaError_t e = launch_stage(sp, strm);
+            if (e == cudaSuccess) e = launch_flash(f, y.d, strm);
+            if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+            return PUZZLEKV_OK;
+        }
         RowsParams rp;
         rows_params(s, layer, rp);
         rp.k_new = static_cast<const char *>(k);

@@ -1,0 +1,728 @@
+// Chunk attention on the fifth-generation tensor cores ("PuzzleKV: Page-Wise
+// Low-Rank Decomposition for KV Cache Compression", §3.3 ④, eqs. (4)-(5)).
+//
+// One pass over the keys in blocks of 128 for 256 query rows at a time: S = Q
+// K^T into tensor memory, the online softmax in registers (one row per
+// thread), P back into tensor memory as the next product's operand, O += P V.
+#include <algorithm>
+
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+namespace {
+
+// Three warpgroups.  Launched with 168 registers a thread (384 x 168 = 64,512),
+// the two softmax warpgroups, which hold a score row each thread, take 224 and
+// the third keeps 56: 2 x 224 + 56 = 3 x 168.
+constexpr int FLASH_THREADS = 384;
+constexpr int RING = 5;  // key / value images in flight: what is left of shared memory beside two query tiles
+
+// The pieces of one CTA's share of the units, in order.
+struct Pieces {
+    const FlashParams &p;
+    long long u, end;
+    int i, h, pair, b0;
+    bool first;
+    // the current piece
+    int ci, ch, cpair, cb0, cb1, cnb;
+    bool cfirst;
+    __device__ __forceinline__ Pieces(const FlashParams &p_, int cta) : p(p_), i(0), h(0), pair(0), first(true) {
+        const long long U = p.unit_off[p.nseq];
+        u = U * cta / p.ctas;
+        end = U * (cta + 1) / p.ctas;
+        if (u >= end) return;
+        while (u >= p.unit_off[i + 1]) ++i;
+        long long r = u - p.unit_off[i];
+        h = (int)(r / p.head_units[i]);
+        r %= p.head_units[i];
+        for (int nb; r >= (nb = flash_blocks(p.T[i], p.n[i], p.G, pair)); ++pair) r -= nb;
+        b0 = (int)r;
+    }
+    __device__ __forceinline__ bool next() {
+        if (u >= end) return false;
+        ci = i; ch = h; cpair = pair; cb0 = b0; cfirst = first;
+        cnb = flash_blocks(p.T[i], p.n[i], p.G, pair);
+        cb1 = (int)min((long long)cnb, b0 + (end - u));
+        u += cb1 - cb0;
+        first = false;
+        b0 = 0;
+        if ((pair + 1) * FLASH_ROWS < p.n[i] * p.G) {
+            ++pair;
+        } else {
+            pair = 0;
+            if (++h == p.H) {
+                h = 0;
+                do ++i;  // entries without units do not occur, but cost nothing here
+                while (i < p.nseq && p.unit_off[i + 1] == p.unit_off[i]);
+            }
+        }
+        return true;
+    }
+    __device__ __forceinline__ int rows() const { return p.n[ci] * p.G; }
+    __device__ __forceinline__ long long image(int b) const {
+        const int nblk = p.blk_off[ci + 1] - p.blk_off[ci];
+        return (long long)p.blk_off[ci] * p.H + (long long)ch * nblk + b;
+    }
+};
+
+struct FlashShared {
+    uint64_t kv_full[RING], kv_empty[RING], q_full[2], s_full[2], p_full[2], o_full[2];
+    uint32_t tmem;
+    volatile int failed;
+};
+
+// Bounded wait of one role; when it gives up, or another role has, every role leaves.
+__device__ __forceinline__ bool role_wait(FlashShared &s, uint64_t *bar, uint32_t parity, int *status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 0) {
+            if (s.failed) return false;
+            if (global_ns() - t0 > WAIT_NS) break;
+        }
+    }
+    s.failed = 1;
+    atomicOr(status + STATUS_TIMEOUT, 1);
+    return false;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A power of two exponent e with |x| 2^-e in [2^12, 2^13) for the largest
+// finite |x| = m (0 for m = 0): fp16 then holds x 2^-e with 11 bits down to
+// 2^-27 of m.  2^e and 2^-e stay normal fp32 numbers.
+__device__ __forceinline__ int fp16_exponent(float m) {
+    if (!(m > 0.f)) return 0;
+    const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127 - 12;
+    return max(-110, min(e, 115));
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ float finite_abs(float x) {
+    const float a = fabsf(x);
+    return a <= 3.4028235e38f ? a : 0.f;  // an infinity or NaN sets no scale
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- operand images
+
+// CTA (entry, head, block of 128 positions): the key and value images.  A
+// factorized page's rows are L_K R_K and (transposed) R_V^T L_V^T, products of
+// the stored bf16 factors with fp32 sums (m16n8k16 on the warps: each product
+// is tiny and its operands lie as stored); dense rows and the chunk's come as
+// they are.  The rows are rounded once, to fp16 scaled by a power of two per
+// block: 11 bits against bf16's 8, because a key's rounding moves its score,
+// and the scores' errors, unlike the output's rounding, grow with |s|.
+// (Rebuilt keys and values in bf16 left 6e-3 of the output's norm at 32K tokens,
+// 3.5 times the output's own rounding.)
+template <int P, int D>
+__global__ void __launch_bounds__(256) stage_kernel(const StageParams p) {
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ uint64_t bar;
+    __shared__ float red[2][8];
+    constexpr int NP = FLASH_KEYS / P, IMG = FLASH_KEYS * D * 2;
+    const Layout &y = p.y;
+    unsigned char *imgK = sm, *imgV = sm + IMG, *recs = sm + 2 * IMG;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    int i = 0;
+    while ((int)blockIdx.x >= p.blk_off[i + 1] * y.H) ++i;
+    const int nblk = p.blk_off[i + 1] - p.blk_off[i];
+    const int u = (int)blockIdx.x - p.blk_off[i] * y.H, h = u / nblk, blk = u % nblk;
+    const int T0 = p.T[i], T1 = T0 + p.n[i], b = p.seqs[i];
+    auto factored = [&](int s) {
+        const int pg = blk * NP + s;
+        return pg * P < T0 && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
+    };
+    bool any = false;
+    for (int s = 0; s < NP; ++s) any |= factored(s);
+    if (any) {
+        if (tid == 0) {
+            mbar_init(&bar, 1);
+            fence_barrier_init();
+            uint32_t tx = 0;
+            for (int s = 0; s < NP; ++s) tx += factored(s) ? (uint32_t)y.rec_bytes : 0u;
+            mbar_arrive_expect_tx(&bar, tx);
+            for (int s = 0; s < NP; ++s)
+                if (factored(s))
+                    bulk_g2s(recs + s * y.rec_bytes, p.factor_pool + y.record_offset(p.layer, b, h, blk * NP + s),
+                             (uint32_t)y.rec_bytes, &bar);
+        }
+        __syncthreads();
+        const bool ok = __syncthreads_and(mbar_wait_bounded(&bar, 0, p.status) ? 1 : 0) != 0;
+        if (!ok) {  // let the copies land, then leave the images as they are
+            if (tid == 0) mbar_wait_bounded(&bar, 0, nullptr);
+            __syncthreads();
+            return;
+        }
+    }
+    const __nv_bfloat16 *knew = reinterpret_cast<const __nv_bfloat16 *>(p.k_new);
+    const __nv_bfloat16 *vnew = reinterpret_cast<const __nv_bfloat16 *>(p.v_new);
+
+    // keys: warp w holds positions 16w .. 16w + 15, all d columns
+    float acc[16][4];
+    {
+        const int s = 16 * warp / P, t0 = 16 * warp % P;
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+        if (factored(s)) {
+            const uint32_t LK = smem_u32(recs + s * y.rec_bytes), RK = LK + (uint32_t)y.off_RK;
+            const int pitch = y.rkp * 2;
+            int k0 = 0;
+            for (; k0 + 16 <= y.rkp; k0 += 16) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(LK + swz_offset(t0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < D / 8; nt += 2) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(RK + swz_offset(k0 + (lane & 15), 16 * nt + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
+                    mma16816(acc[nt], a0, a1, a2, a3, b0, b1);
+                    mma16816(acc[nt + 1], a0, a1, a2, a3, b2, b3);
+                }
+            }
+            if (k0 < y.rkp) {  // eight ranks left
+                uint32_t a0, a1;
+                ldsm_x2(LK + swz_offset(t0 + (lane & 15), 2 * k0, pitch), a0, a1);
+#pragma unroll
+                for (int nt = 0; nt < D / 8; nt += 4) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(RK + swz_offset(k0 + (lane & 7), 16 * nt + 16 * (lane >> 3), D * 2), b0, b1, b2, b3);
+                    mma1688(acc[nt], a0, a1, b0);
+                    mma1688(acc[nt + 1], a0, a1, b1);
+                    mma1688(acc[nt + 2], a0, a1, b2);
+                    mma1688(acc[nt + 3], a0, a1, b3);
+                }
+            }
+        } else {
+            const int pg = blk * NP + s;
+            const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, 0);
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2) {
+                const int t = t0 + g + 8 * r2, pos = pg * P + t;
+                if (pos >= T1) continue;
+#pragma unroll
+                for (int nt = 0; nt < D / 8; ++nt) {
+                    const int col = 8 * nt + 2 * c;
+                    const __nv_bfloat16 *src = pos < T0 ? swz_ptr<__nv_bfloat16>(page, t, col, D)
+                                                        : knew + ((size_t)(p.off[i] + pos - T0) * y.H + h) * D + col;
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(src);
+                    acc[nt][2 * r2] = bf16_lo_to_f32(v);
+                    acc[nt][2 * r2 + 1] = bf16_hi_to_f32(v);
+                }
+            }
+        }
+        if (y.rope) {  // turn each pair of columns (j, j + d/2) by its position
+            const int pg = blk * NP + s;
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2) {
+                const int t = t0 + g + 8 * r2;
+                if (pg * P + t >= T1) continue;
+#pragma unroll
+                for (int nt = 0; nt < D / 16; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 8 * nt + 2 * c + e;
+                        const float2 a = p.rope_base[(size_t)pg * (D / 2) + j], o = p.rope_delta[t * (D / 2) + j];
+                        const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
+                        float &x0 = acc[nt][2 * r2 + e], &x1 = acc[nt + D / 16][2 * r2 + e];
+                        const float u0 = x0 * cs - x1 * sn, u1 = x1 * cs + x0 * sn;
+                        x0 = u0;
+                        x1 = u1;
+                    }
+            }
+        }
+    }
+    auto block_max = [&](int which, int tiles) {
+        float m = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < 16; ++nt)
+            if (nt < tiles)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m = fmaxf(m, finite_abs(acc[nt][e]));
+        m = warp_max(m);
+        if (lane == 0) red[which][warp] = m;
+        __syncthreads();
+        m = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[which][w]);
+        return m;
+    };
+    const int ek = fp16_exponent(block_max(0, D / 8));
+    {
+        const float f = pow2i(-ek);
+#pragma unroll
+        for (int nt = 0; nt < D / 8; ++nt)
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2) {
+                const int r = 16 * warp + g + 8 * r2;
+                *reinterpret_cast<uint32_t *>(imgK + (nt / 8) * (FLASH_KEYS * 128) + r * 128 + (((nt & 7) ^ (r & 7)) << 4) +
+                                              4 * c) = pack_f16(acc[nt][2 * r2] * f, acc[nt][2 * r2 + 1] * f);
+            }
+    }
+
+    // values, transposed: 16 head dimensions per warp; all 128 positions at D =
+    // 128, one half of them at D = 64
+    constexpr int VT = D == 128 ? 16 : 8;
+    const int d0 = 16 * (warp % (D / 16)), key0 = D == 128 ? 0 : 64 * (warp / 4);
+#pragma unroll
+    for (int nt = 0; nt < VT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+    for (int s2 = 0; s2 < 8 * VT / P; ++s2) {
+        const int s = key0 / P + s2;
+        constexpr int PT = P / 8;  // position tiles of a page
+        if (factored(s)) {
+            const uint32_t LV = smem_u32(recs + s * y.rec_bytes) + (uint32_t)y.off_LV;
+            const uint32_t RV = smem_u32(recs + s * y.rec_bytes) + (uint32_t)y.off_RV;
+            const int pitch = y.rvp * 2;
+            int k0 = 0;
+            for (; k0 + 16 <= y.rvp; k0 += 16) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(RV + swz_offset(d0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+#pragma unroll
+                for (int nt = 0; nt < PT; nt += 2) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4_t(LV + swz_offset(k0 + (lane & 15), 16 * nt + 16 * (lane >> 4), P * 2), b0, b1, b2, b3);
+                    mma16816(acc[s2 * PT + nt], a0, a1, a2, a3, b0, b1);
+                    mma16816(acc[s2 * PT + nt + 1], a0, a1, a2, a3, b2, b3);
+                }
+            }
+            if (k0 < y.rvp) {
+                uint32_t a0, a1;
+                ldsm_x2(RV + swz_offset(d0 + (lane & 15), 2 * k0, pitch), a0, a1);
+#pragma unroll
+                for (int nt = 0; nt < PT; nt += 2) {
+                    uint32_t b0, b1;
+                    const int row = k0 + (lane & 7), col = 16 * nt + 16 * ((lane >> 3) & 1);
+                    uint32_t addr = LV + swz_offset(row, col, P * 2);
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                                 : "=r"(b0), "=r"(b1) : "r"(addr));
+                    mma1688(acc[s2 * PT + nt], a0, a1, b0);
+                    mma1688(acc[s2 * PT + nt + 1], a0, a1, b1);
+                }
+            }
+        } else {
+            const int pg = blk * NP + s;
+            const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, 1);
+#pragma unroll
+            for (int nt = 0; nt < PT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 8 * nt + 2 * c + (e & 1), pos = pg * P + t, dim = d0 + g + 8 * (e >> 1);
+                    if (pos >= T1) continue;
+                    const __nv_bfloat16 *src = pos < T0 ? swz_ptr<__nv_bfloat16>(page, t, dim, D)
+                                                        : vnew + ((size_t)(p.off[i] + pos - T0) * y.H + h) * D + dim;
+                    acc[s2 * PT + nt][e] = __bfloat162float(*src);
+                }
+        }
+    }
+    // values of ordinary size keep scale 1, so that a sequence's blocks agree
+    const float vmax = block_max(1, VT);
+    const int ev = vmax > 0.f && (vmax >= 32768.f || vmax < 0.00390625f) ? fp16_exponent(vmax) : 0;
+    {
+        const float f = pow2i(-ev);
+#pragma unroll
+        for (int nt = 0; nt < VT; ++nt)
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2) {
+                const int r = d0 + g + 8 * r2, key = key0 + 8 * nt;
+                *reinterpret_cast<uint32_t *>(imgV + (key / 64) * (D * 128) + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4) +
+                                              4 * c) = pack_f16(acc[nt][2 * r2] * f, acc[nt][2 * r2 + 1] * f);
+            }
+    }
+    fence_proxy_async_shared();
+    __syncthreads();
+    if (tid == 0) {
+        char *dst = p.images + (size_t)blockIdx.x * (2 * IMG);
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(imgK)),
+                     "r"((uint32_t)(2 * IMG))
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        p.scales[blockIdx.x] = make_float2((float)ek, (float)ev);
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------------- attention
+
+// Warps 0-3 and 4-7: the softmax of one 128-row tile each (thread = row); warp
+// 8: the matrix products; warp 9: the copies.  Tensor memory: the tiles' S (128
+// columns each; P overwrites it as fp16 in the first 64), then their O.
+//
+// Order of the products: S0(0) S1(0), then per block PV0 S0' PV1 S1', so that
+// while one tile's softmax runs, the other tile's two products do.  A commit
+// covers every product issued before it: when a tile's S is complete, so is
+// its previous P V, and its threads may rescale O.
+template <int D>
+__global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashParams p) {
+    extern __shared__ unsigned char sm_raw[];
+    __shared__ FlashShared s;
+    constexpr int IMG = FLASH_KEYS * D * 2;  // a key image, a value image, a query tile
+    unsigned char *sm = sm_raw + ((1024 - (smem_u32(sm_raw) & 1023)) & 1023);
+    unsigned char *Qs = sm, *ring = sm + 2 * IMG;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < RING; ++k) {
+            mbar_init(&s.kv_full[k], 1);
+            mbar_init(&s.kv_empty[k], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s.q_full[t], 128);
+            mbar_init(&s.s_full[t], 1);
+            mbar_init(&s.p_full[t], 128);
+            mbar_init(&s.o_full[t], 1);
+        }
+        s.failed = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) tmem_alloc(&s.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    Pieces pc(p, blockIdx.x);
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        const int t = warp >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+        const uint32_t lanes = (uint32_t)(32 * w4) << 16;
+        const uint32_t tS = tmem + lanes + 128 * t, tO = tmem + lanes + 256 + 128 * t;
+        unsigned char *q_tile = Qs + t * IMG;
+        uint32_t s_phase = 0, o_phase = 0;
+        while (pc.next()) {
+            const int R = pc.rows(), r0 = pc.cpair * FLASH_ROWS + 128 * t;
+            if (r0 >= R) continue;
+            const int r = r0 + row, i = pc.ci, G = p.G;
+            const bool live = r < R;
+            const int tok = (live ? r : R - 1) / G, lim = p.T[i] + tok;
+            // the query row: fp16, scaled by a power of two of its own
+            float qs;
+            {
+                uint4 v[D / 8];
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.q + (((size_t)(p.off[i] + tok) * p.Hq + pc.ch * G + (live ? r % G : 0)) * D) * 2);
+                float m = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) v[k] = live ? src[k] : make_uint4(0, 0, 0, 0);
+                auto each = [&](uint32_t w) {
+                    m = fmaxf(m, fmaxf(finite_abs(bf16_lo_to_f32(w)), finite_abs(bf16_hi_to_f32(w))));
+                };
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    each(v[k].x);
+                    each(v[k].y);
+                    each(v[k].z);
+                    each(v[k].w);
+                }
+                const int e = fp16_exponent(m);
+                const float f = pow2i(-e);
+                qs = pow2i(e) * p.scale_log2;
+                auto cv = [&](uint32_t w) { return pack_f16(bf16_lo_to_f32(w) * f, bf16_hi_to_f32(w) * f); };
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k)
+                    *reinterpret_cast<uint4 *>(q_tile + (k / 8) * (128 * 128) + row * 128 + (((k & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(cv(v[k].x), cv(v[k].y), cv(v[k].z), cv(v[k].w));
+            }
+            fence_proxy_async_shared();
+            tc_fence_before();  // the previous piece's O has been read
+            mbar_arrive(&s.q_full[t]);
+            float m = -INFINITY, l = 0.f;
+            int E = 0;
+            const float2 *scales = p.scales + pc.image(0);
+            float2 sc = scales[pc.cb0];
+            const int full = (p.T[i] + r0 / G + 1) / FLASH_KEYS;  // blocks before it are seen whole by every row of the tile
+            bool ok = true;
+            for (int blk = pc.cb0; blk < pc.cb1; ++blk) {
+                const float cf = qs * pow2i((int)sc.x);
+                const int ev = (int)sc.y;
+                if (blk + 1 < pc.cb1) sc = scales[blk + 1];
+                // a warp leaves as one: tensor-memory accesses are whole-warp operations
+                if (!(ok = __all_sync(0xffffffffu, role_wait(s, &s.s_full[t], s_phase, p.status)))) break;
+                s_phase ^= 1;
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_ld32(tS + 32 * k, x[k]);
+                tc_wait_ld();
+                if (blk >= full) {
+                    const int last = lim - blk * FLASH_KEYS;  // last column this row sees
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * k + e > last) x[k][e] = 0xff800000u;
+                }
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[k][e]));
+                mx *= cf;
+                // The reference m moves only when a score exceeds it by 2^8 (the
+                // weights then stay below 2^8, far inside fp16), so O is rescaled
+                // rarely; a value block of a larger scale rescales it as well.
+                float f = 1.f;
+                if (blk == pc.cb0) {
+                    m = mx;
+                    E = ev;
+                } else {
+                    if (mx > m + 8.f) {
+                        f = m == -INFINITY ? 1.f : ex2(m - mx);
+                        m = mx;
+                        l *= f;
+                    }
+                    if (ev > E) {
+                        f *= pow2i(max(E - ev, -126));
+                        E = ev;
+                    }
+                    if (__any_sync(0xffffffffu, f != 1.f)) {
+                        for (int k = 0; k < D / 32; ++k) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32 * k, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(tO + 32 * k, o);
+                        }
+                    }
+                }
+                const float up = (float)max(ev - E, -120);  // 2^up: this block's values in units of O
+                const float off = (m == -INFINITY ? 0.f : m) - up;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float p0 = ex2(fmaf(__uint_as_float(x[2 * k + e / 16][(2 * e) & 31]), cf, -off));
+                        const float p1 = ex2(fmaf(__uint_as_float(x[2 * k + e / 16][(2 * e + 1) & 31]), cf, -off));
+                        sum[e & 3] += p0 + p1;
+                        w[e] = pack_f16(p0, p1);
+                    }
+                    tmem_st32(tS + 32 * k, w);
+                }
+                const float ls = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += up == 0.f ? ls : ls * ex2(-up);
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(&s.p_full[t]);
+            }
+            if (!ok || !__all_sync(0xffffffffu, role_wait(s, &s.o_full[t], o_phase, p.status))) break;
+            o_phase ^= 1;
+            tc_fence_after();
+            const float unit = pow2i(E);
+            const bool whole = pc.cb0 == 0 && pc.cb1 == pc.cnb;
+            const float f = whole ? unit / l : unit;
+            float *part = nullptr;
+            if (!whole) {
+                part = p.partials + ((size_t)(2 * blockIdx.x + (pc.cfirst ? 0 : 1)) * FLASH_ROWS + 128 * t + row) * (D + 4);
+                if (live) *reinterpret_cast<float4 *>(part) = make_float4(m, l, 0.f, 0.f);
+            }
+            char *out = p.out + (((size_t)(p.off[i] + tok) * p.Hq + pc.ch * G + r % G) * D) * 2;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * k, o);
+                tc_wait_ld();
+                if (!live) continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        auto pk = [&](int a) {
+                            return pack_bf16(__uint_as_float(o[e + a]) * f, __uint_as_float(o[e + a + 1]) * f);
+                        };
+                        *reinterpret_cast<uint4 *>(out + (32 * k + e) * 2) = make_uint4(pk(0), pk(2), pk(4), pk(6));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(part + 4 + 32 * k + e) =
+                            make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                        __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                }
+            }
+        }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 8) {
+        if (lane == 0) {
+            const uint32_t q0 = smem_u32(Qs), r0 = smem_u32(ring);
+            constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
+            uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto full = [&](uint32_t n) { return role_wait(s, &s.kv_full[n % RING], (n / RING) & 1, p.status); };
+            auto scores = [&](int t, uint32_t n) {
+                const uint32_t a = q0 + t * IMG, b = r0 + (n % RING) * IMG;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    tc_mma_ss(tmem + 128 * t, tc_desc(a + (k / 4) * (128 * 128) + (k % 4) * 32),
+                              tc_desc(b + (k / 4) * (FLASH_KEYS * 128) + (k % 4) * 32), ID_S, k > 0);
+                tc_commit(&s.s_full[t]);
+            };
+            auto values = [&](int t, uint32_t n, bool acc) {
+                const uint32_t b = r0 + (n % RING) * IMG;
+#pragma unroll
+                for (int k = 0; k < FLASH_KEYS / 16; ++k)
+                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, tc_desc(b + (k / 4) * (D * 128) + (k % 4) * 32),
+                              ID_O, acc || k > 0);
+            };
+            while (ok && pc.next()) {
+                const int tiles = pc.cpair * FLASH_ROWS + 128 < pc.rows() ? 2 : 1, nb = pc.cb1 - pc.cb0;
+                for (int t = 0; t < tiles && ok; ++t) {
+                    ok = role_wait(s, &s.q_full[t], q_phase[t], p.status);
+                    q_phase[t] ^= 1;
+                }
+                ok = ok && full(x);
+                if (!ok) break;
+                tc_fence_after();
+                for (int t = 0; t < tiles; ++t) scores(t, x);
+                tc_commit(&s.kv_empty[x % RING]);
+                for (int j = 0; j < nb && ok; ++j) {
+                    const uint32_t v = x + 1 + 2 * j;
+                    const bool more = j + 1 < nb;
+                    ok = full(v) && (!more || full(v + 1));
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        ok = role_wait(s, &s.p_full[t], p_phase[t], p.status);
+                        if (!ok) break;
+                        p_phase[t] ^= 1;
+                        tc_fence_after();
+                        values(t, v, j > 0);
+                        if (more)
+                            scores(t, v + 1);
+                        else
+                            tc_commit(&s.o_full[t]);
+                    }
+                    tc_commit(&s.kv_empty[v % RING]);
+                    if (more) tc_commit(&s.kv_empty[(v + 1) % RING]);
+                }
+                x += 2 * nb;
+            }
+            if (!ok) {  // products still in flight end before the tensor memory is freed
+                tc_commit(&s.q_full[0]);
+                for (int k = 0; k < 1000 && s.failed; ++k) __nanosleep(1000);
+            }
+        }
+      } else if (warp == 9) {
+        if (lane == 0) {
+            uint32_t x = 0;
+            bool ok = true;
+            while (ok && pc.next()) {
+                const char *src = p.images + (size_t)pc.image(pc.cb0) * (2 * IMG);
+                for (int k = 0; k < 2 * (pc.cb1 - pc.cb0) && ok; ++k, ++x) {
+                    ok = role_wait(s, &s.kv_empty[x % RING], ((x / RING) & 1) ^ 1, p.status);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&s.kv_full[x % RING], IMG);
+                    bulk_g2s(ring + (x % RING) * IMG, src + (size_t)k * IMG, IMG, &s.kv_full[x % RING]);
+                }
+            }
+            if (!ok)  // copies still in flight land before the CTA ends
+                for (uint32_t k = x < RING ? 0 : x - RING; k < x; ++k)
+                    mbar_wait_bounded(&s.kv_full[k % RING], (k / RING) & 1, nullptr);
+        }
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_free(tmem, 512);
+}
+
+// Join the states of pairs cut between CTAs, eq. (5): block (pair, group of 32
+// rows), one warp per row, pieces in order (the same sums in every launch).
+template <int D>
+__global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the pair, by its number over all entries
+    int i = 0, u = blockIdx.x;
+    for (; i < p.nseq; ++i) {
+        const int here = (p.n[i] * p.G + FLASH_ROWS - 1) / FLASH_ROWS * p.H;
+        if (u < here) break;
+        u -= here;
+    }
+    const int R = p.n[i] * p.G, pairs = (R + FLASH_ROWS - 1) / FLASH_ROWS, h = u / pairs, pair = u % pairs;
+    long long u0 = p.unit_off[i] + h * p.head_units[i];
+    for (int k = 0; k < pair; ++k) u0 += flash_blocks(p.T[i], p.n[i], p.G, k);
+    const long long u1 = u0 + flash_blocks(p.T[i], p.n[i], p.G, pair), U = p.unit_off[p.nseq];
+    auto owner = [&](long long x) {  // the CTA whose share [U c / ctas, U (c + 1) / ctas) holds unit x
+        int c = (int)(x * p.ctas / U);
+        while (U * (c + 1) / p.ctas <= x) ++c;
+        while (U * c / p.ctas > x) --c;
+        return c;
+    };
+    const int c0 = owner(u0), c1 = owner(u1 - 1);
+    if (c0 == c1) return;
+    const int slot0 = U * c0 / p.ctas == u0 ? 2 * c0 : 2 * c0 + 1;
+    constexpr int V = D / 32;
+    for (int k = warp; k < 32; k += 8) {
+        const int rr = 32 * blockIdx.y + k, r = pair * FLASH_ROWS + rr;
+        if (r >= R) break;
+        auto row = [&](int c) { return p.partials + ((size_t)(c == c0 ? slot0 : 2 * c) * FLASH_ROWS + rr) * (D + 4); };
+        float M = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, row(c)[0]);
+        M = warp_max(M);
+        float L = 0.f, acc[V] = {};
+        for (int c = c0; c <= c1; ++c) {
+            const float *q = row(c);
+            const float f = ex2(q[0] - M);
+            L = fmaf(f, q[1], L);
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = fmaf(f, q[4 + lane * V + j], acc[j]);
+        }
+        const float il = 1.f / L;
+        __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) +
+                             ((size_t)(p.off[i] + r / p.G) * p.Hq + h * p.G + r % p.G) * D;
+#pragma unroll
+        for (int j = 0; j < V; ++j) dst[lane * V + j] = __float2bfloat16_rn(acc[j] * il);
+    }
+}
+
+template <int P, int D>
+static cudaError_t stage_t(const StageParams &p, cudaStream_t st) {
+    const int smem = 2 * FLASH_KEYS * D * 2 + FLASH_KEYS / P * (int)p.y.rec_bytes;
+    cudaError_t e = cudaFuncSetAttribute(stage_kernel<P, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    stage_kernel<P, D><<<(unsigned)(p.blk_off[p.nseq] * p.y.H), 256, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_stage(const StageParams &p, cudaStream_t st) {
+    if (p.blk_off[p.nseq] == 0) return cudaSuccess;
+    if (p.y.d == 64) {
+        if (p.y.P == 16) return stage_t<16, 64>(p, st);
+        if (p.y.P == 32) return stage_t<32, 64>(p, st);
+        return stage_t<64, 64>(p, st);
+    }
+    if (p.y.P == 16) return stage_t<16, 128>(p, st);
+    if (p.y.P == 32) return stage_t<32, 128>(p, st);
+    return stage_t<64, 128>(p, st);
+}
+
+template <int D>
+static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
+    constexpr int smem = (2 + RING) * FLASH_KEYS * D * 2 + 1024;
+    cudaError_t e = cudaFuncSetAttribute(flash_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    flash_kernel<D><<<(unsigned)p.ctas, FLASH_THREADS, smem, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.ctas == 1) return e;
+    int pairs = 0, most = 0;
+    for (int i = 0; i < p.nseq; ++i) {
+        pairs += (p.n[i] * p.G + FLASH_ROWS - 1) / FLASH_ROWS * p.H;
+        most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
+    }
+    flash_merge_kernel<D><<<dim3((unsigned)pairs, (unsigned)((most + 31) / 32)), 256, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st) {
+    if (p.unit_off[p.nseq] == 0) return cudaSuccess;
+    return d == 64 ? flash_t<64>(p, st) : flash_t<128>(p, st);
+}
+
+}  // namespace pkv

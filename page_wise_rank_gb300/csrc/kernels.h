@@ -190,6 +190,52 @@ struct ChunkAttnParams {
     int tile_off[MAX_CALL_BATCH + 1];  // CTAs of the entries before (filled by the launcher)
 };
 
+// Chunk attention on the fifth-generation tensor cores (bf16 stores).  The
+// entries' rows 0 .. T + n - 1 are laid out as fp16 operand images, one pair
+// (keys [128][d], values transposed [d][128], both K-major in the 128-byte
+// swizzle) per KV head and block of 128 positions: entry i, head h, block b at
+// index (blk_off[i] H + h nblk(i) + b), nblk(i) = ceil((T[i] + n[i]) / 128).
+// scales holds each block's powers of two (key, value): row = image 2^scale.
+struct StageParams {
+    Layout y;
+    const char *factor_pool, *dense_pool;
+    const float2 *rope_base, *rope_delta;
+    const char *k_new, *v_new;
+    char *images;
+    float2 *scales;
+    int *status;
+    int layer, nseq;
+    int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH];
+    int blk_off[MAX_CALL_BATCH + 1];
+};
+
+// The query rows of (entry, KV head) are cut into pairs of 128-row tiles; pair
+// p attends blocks 0 .. flash_blocks() - 1.  All (entry, head, pair, block)
+// units in this order are shared out evenly over ctas CTAs; the states of
+// pairs cut between CTAs go to partials ([2 ctas][256][d + 4]).
+struct FlashParams {
+    int H, Hq, G, nseq, ctas;
+    float scale_log2;
+    const char *q;
+    char *out;
+    const char *images;
+    const float2 *scales;
+    float *partials;
+    int *status;
+    int T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH], blk_off[MAX_CALL_BATCH + 1];
+    long long head_units[MAX_CALL_BATCH], unit_off[MAX_CALL_BATCH + 1];
+};
+constexpr int FLASH_ROWS = 256, FLASH_KEYS = 128;  // query rows of a pair of tiles, keys of a block
+
+// Blocks that pair p of an entry of T cached and n new tokens attends.
+PKV_HD int flash_blocks(int T, int n, int G, int p) {
+    const int last = (p + 1) * FLASH_ROWS < n * G ? (p + 1) * FLASH_ROWS : n * G;
+    return (T + (last - 1) / G) / FLASH_KEYS + 1;
+}
+
+cudaError_t launch_stage(const StageParams &p, cudaStream_t st);
+cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st);
+
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st);
 cudaError_t launch_append_chunk(const AppendChunkParams &p, cudaStream_t st);
 cudaError_t launch_truncate(const TruncateParams &p, cudaStream_t st);
