@@ -95,6 +95,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // A power of two exponent e with |x| 2^-e in [2^12, 2^13) for the largest
 // finite |x| = m (0 for m = 0): fp16 then holds x 2^-e with 11 bits down to
 // 2^-27 of m.  2^e and 2^-e stay normal fp32 numbers.
@@ -457,11 +477,21 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                         for (int e = 0; e < 32; ++e)
                             if (32 * k + e > last) x[k][e] = 0xff800000u;
                 }
-                float mx = -INFINITY;
+                float mx;
+                {  // eight short chains of three-input maxima
+                    float a[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                    for (int e = 0; e < 8; ++e) a[e] = __uint_as_float(x[0][e]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[k][e]));
+                    for (int e = 8; e < 128; e += 16)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float v0 = __uint_as_float(x[(e + j) / 32][(e + j) & 31]);
+                            const float v1 = e + 8 + j < 128 ? __uint_as_float(x[((e + 8 + j) / 32) & 3][(e + 8 + j) & 31]) : v0;
+                            a[j] = fmaxf(fmaxf(a[j], v0), v1);
+                        }
+                    mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+                }
                 mx *= cf;
                 // The reference m moves only when a score exceeds it by 2^8 (the
                 // weights then stay below 2^8, far inside fp16), so O is rescaled
@@ -493,20 +523,26 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 }
                 const float up = (float)max(ev - E, -120);  // 2^up: this block's values in units of O
                 const float off = (m == -INFINITY ? 0.f : m) - up;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint64_t sum[2] = {0, 0};  // pairs of zeros
+                const uint64_t cf2 = pair(cf, cf), off2 = pair(-off, -off);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     uint32_t w[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const float p0 = ex2(fmaf(__uint_as_float(x[2 * k + e / 16][(2 * e) & 31]), cf, -off));
-                        const float p1 = ex2(fmaf(__uint_as_float(x[2 * k + e / 16][(2 * e + 1) & 31]), cf, -off));
-                        sum[e & 3] += p0 + p1;
+                        const uint32_t *xx = &x[2 * k + e / 16][(2 * e) & 31];
+                        float p0, p1;
+                        unpair(fma2(pair(__uint_as_float(xx[0]), __uint_as_float(xx[1])), cf2, off2), p0, p1);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
                         w[e] = pack_f16(p0, p1);
                     }
                     tmem_st32(tS + 32 * k, w);
                 }
-                const float ls = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float ls, ls1;
+                unpair(add2(sum[0], sum[1]), ls, ls1);
+                ls += ls1;
                 l += up == 0.f ? ls : ls * ex2(-up);
                 tc_wait_st();
                 tc_fence_before();
@@ -550,63 +586,75 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp == 8) {
-        if (lane == 0) {
-            const uint32_t q0 = smem_u32(Qs), r0 = smem_u32(ring);
-            constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
-            uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-            bool ok = true;
-            auto full = [&](uint32_t n) { return role_wait(s, &s.kv_full[n % RING], (n / RING) & 1, p.status); };
-            auto scores = [&](int t, uint32_t n) {
-                const uint32_t a = q0 + t * IMG, b = r0 + (n % RING) * IMG;
+        // One elected lane issues, but the whole warp runs the loop: addresses
+        // and descriptors then stay in uniform registers.  With a single lane
+        // in the loop each product took 90-107 cycles to issue against the 64
+        // it runs for.
+        const uint32_t leader = elect_one();
+        const uint64_t dq = tc_desc(smem_u32(Qs)), dr = tc_desc(smem_u32(ring));
+        constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
+        uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, role_wait(s, bar, parity, p.status)) != 0; };
+        auto full = [&](uint32_t n) { return wait(&s.kv_full[n % RING], (n / RING) & 1); };
+        auto scores = [&](int t, uint32_t n) {
+            const uint64_t a = dq + t * (IMG >> 4), b = dr + (n % RING) * (IMG >> 4);
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ss(tmem + 128 * t, tc_desc(a + (k / 4) * (128 * 128) + (k % 4) * 32),
-                              tc_desc(b + (k / 4) * (FLASH_KEYS * 128) + (k % 4) * 32), ID_S, k > 0);
+                    tc_mma_ss(tmem + 128 * t, a + (k / 4) * (128 * 128 >> 4) + (k % 4) * 2,
+                              b + (k / 4) * (FLASH_KEYS * 128 >> 4) + (k % 4) * 2, ID_S, k > 0);
                 tc_commit(&s.s_full[t]);
-            };
-            auto values = [&](int t, uint32_t n, bool acc) {
-                const uint32_t b = r0 + (n % RING) * IMG;
+            }
+            __syncwarp();
+        };
+        auto values = [&](int t, uint32_t n, bool acc) {
+            const uint64_t b = dr + (n % RING) * (IMG >> 4);
+            if (leader) {
 #pragma unroll
                 for (int k = 0; k < FLASH_KEYS / 16; ++k)
-                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, tc_desc(b + (k / 4) * (D * 128) + (k % 4) * 32),
-                              ID_O, acc || k > 0);
-            };
-            while (ok && pc.next()) {
-                const int tiles = pc.cpair * FLASH_ROWS + 128 < pc.rows() ? 2 : 1, nb = pc.cb1 - pc.cb0;
+                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + (k / 4) * (D * 128 >> 4) + (k % 4) * 2, ID_O,
+                              acc || k > 0);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint64_t *bar) {
+            if (leader) tc_commit(bar);
+            __syncwarp();
+        };
+        while (ok && pc.next()) {
+            const int tiles = pc.cpair * FLASH_ROWS + 128 < pc.rows() ? 2 : 1, nb = pc.cb1 - pc.cb0;
+            for (int t = 0; t < tiles && ok; ++t) {
+                ok = wait(&s.q_full[t], q_phase[t]);
+                q_phase[t] ^= 1;
+            }
+            ok = ok && full(x);
+            if (!ok) break;
+            tc_fence_after();
+            for (int t = 0; t < tiles; ++t) scores(t, x);
+            commit(&s.kv_empty[x % RING]);
+            for (int j = 0; j < nb && ok; ++j) {
+                const uint32_t v = x + 1 + 2 * j;
+                const bool more = j + 1 < nb;
+                ok = full(v) && (!more || full(v + 1));
                 for (int t = 0; t < tiles && ok; ++t) {
-                    ok = role_wait(s, &s.q_full[t], q_phase[t], p.status);
-                    q_phase[t] ^= 1;
+                    ok = wait(&s.p_full[t], p_phase[t]);
+                    if (!ok) break;
+                    p_phase[t] ^= 1;
+                    tc_fence_after();
+                    values(t, v, j > 0);
+                    if (more)
+                        scores(t, v + 1);
+                    else
+                        commit(&s.o_full[t]);
                 }
-                ok = ok && full(x);
-                if (!ok) break;
-                tc_fence_after();
-                for (int t = 0; t < tiles; ++t) scores(t, x);
-                tc_commit(&s.kv_empty[x % RING]);
-                for (int j = 0; j < nb && ok; ++j) {
-                    const uint32_t v = x + 1 + 2 * j;
-                    const bool more = j + 1 < nb;
-                    ok = full(v) && (!more || full(v + 1));
-                    for (int t = 0; t < tiles && ok; ++t) {
-                        ok = role_wait(s, &s.p_full[t], p_phase[t], p.status);
-                        if (!ok) break;
-                        p_phase[t] ^= 1;
-                        tc_fence_after();
-                        values(t, v, j > 0);
-                        if (more)
-                            scores(t, v + 1);
-                        else
-                            tc_commit(&s.o_full[t]);
-                    }
-                    tc_commit(&s.kv_empty[v % RING]);
-                    if (more) tc_commit(&s.kv_empty[(v + 1) % RING]);
-                }
-                x += 2 * nb;
+                commit(&s.kv_empty[v % RING]);
+                if (more) commit(&s.kv_empty[(v + 1) % RING]);
             }
-            if (!ok) {  // products still in flight end before the tensor memory is freed
-                tc_commit(&s.q_full[0]);
-                for (int k = 0; k < 1000 && s.failed; ++k) __nanosleep(1000);
-            }
+            x += 2 * nb;
         }
+        if (!ok)  // products still in flight end before the tensor memory is freed
+            for (int k = 0; k < 1000; ++k) __nanosleep(1000);
       } else if (warp == 9) {
         if (lane == 0) {
             uint32_t x = 0;
