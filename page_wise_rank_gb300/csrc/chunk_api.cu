@@ -75,6 +75,13 @@ puzzlekv_status check_chunk(const puzzlekv_store *s, int32_t layer, const int32_
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// First dense page past the sink of a T-token sequence (pages [sink, it) are factorized).
+int first_window_page(const Layout &y, int T) {
+    int fw = (T + y.P - 1) / y.P;
+    while (fw > y.sink_pages && page_kind(fw - 1, T, y.P, y.sink_tokens, y.W) == KIND_DENSE) --fw;
+    return fw;
+}
+
 // What a chunk attention call places in its workspace.
 struct AttnPlan {
     ChunkAttnParams a{};  // fp32 and INT4 stores
@@ -98,12 +105,28 @@ void plan_flash(const puzzlekv_store *s, AttnPlan &pl) {
         f.n[j] = a.n[j];
         f.off[j] = a.off[j];
         f.blk_off[j + 1] = f.blk_off[j] + (a.T[j] + a.n[j] + FLASH_KEYS - 1) / FLASH_KEYS;
-        long long u = 0;
-        for (int p = 0; (long long)p * FLASH_ROWS < (long long)a.n[j] * a.G; ++p) u += flash_blocks(a.T[j], a.n[j], a.G, p);
-        f.head_units[j] = u;
-        f.unit_off[j + 1] = f.unit_off[j] + u * a.H;
     }
-    f.ctas = (int)std::min<long long>(s->num_sms, std::max(1LL, f.unit_off[f.nseq]));
+    // units before each pair of every entry, one head
+    std::vector<std::vector<long long>> before(a.nseq);
+    std::vector<long long> head_off;  // units before (entry, head), in order
+    long long U = 0;
+    for (int j = 0; j < a.nseq; ++j) {
+        std::vector<long long> &u = before[j];
+        u.push_back(0);
+        for (int p = 0; (long long)p * FLASH_ROWS < (long long)a.n[j] * a.G; ++p)
+            u.push_back(u.back() + flash_blocks(a.T[j], a.n[j], a.G, p));
+        for (int h = 0; h < a.H; ++h, U += u.back()) head_off.push_back(U);
+    }
+    f.units = U;
+    f.ctas = (int)std::min<long long>(std::min(s->num_sms, FLASH_MAX_CTAS), std::max(1LL, U));
+    for (int c = 0; c < f.ctas; ++c) {
+        const long long u0 = U * c / f.ctas, u1 = U * (c + 1) / f.ctas;
+        const int eh = (int)(std::upper_bound(head_off.begin(), head_off.end(), u0) - head_off.begin()) - 1;
+        const std::vector<long long> &u = before[eh / a.H];
+        const long long r = u0 - head_off[eh];
+        const int pair = (int)(std::upper_bound(u.begin(), u.end(), r) - u.begin()) - 1;
+        f.share[c] = {eh / a.H, eh % a.H, pair, (int)(r - u[pair]), (int)(u1 - u0)};
+    }
     const size_t blocks = (size_t)f.blk_off[f.nseq] * y.H;
     pl.scale_off = blocks * (2 * FLASH_KEYS * y.d * 2);
     pl.part_off = pl.scale_off + up256(blocks * sizeof(float2));
@@ -133,6 +156,7 @@ void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_i
         }
         off += n;
     }
+    if (a.nseq == 0) return;
     if (y.dtype == 1 && !y.q4) {
         pl.flash = true;
         plan_flash(s, pl);
@@ -264,6 +288,7 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
                 sp.T[j] = a.T[j];
                 sp.n[j] = a.n[j];
                 sp.off[j] = a.off[j];
+                sp.fw[j] = first_window_page(y, a.T[j]);
                 sp.blk_off[j + 1] = pl.f.blk_off[j + 1];
             }
             FlashParams &f = pl.f;
@@ -274,7 +299,7 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
             f.partials = reinterpret_cast<float *>(w + pl.part_off);
             f.status = status_ptr(s);
             s->after_decode = false;
-            cudaError_t e = launch_stage(sp, strm);
+            cudaError_t e = launch_stage(sp, s->num_sms, strm);
             if (e == cudaSuccess) e = launch_flash(f, y.d, strm);
             if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
             return PUZZLEKV_OK;
@@ -617,9 +642,7 @@ puzzlekv_status puzzlekv_truncate_sequences(puzzlekv_store *s, const int32_t *se
         for (int i = 0; i < B; ++i) {
             const int b = seq_ids[i], T = lengths[i];
             if (T < 0) return fail(PUZZLEKV_ERR_INVALID_ARG, "lengths[%d] is negative", i);
-            const int pages = (T + y.P - 1) / y.P;
-            int fw = pages;  // first dense page of the shorter sequence past its sink
-            while (fw > y.sink_pages && page_kind(fw - 1, T, y.P, y.sink_tokens, y.W) == KIND_DENSE) --fw;
+            const int pages = (T + y.P - 1) / y.P, fw = first_window_page(y, T);
             for (int l = 0; l < y.L; ++l) {
                 const int have = length_of(s, b, l);
                 if (T > have)

@@ -22,31 +22,22 @@ constexpr int RING = 5;  // key / value images in flight: what is left of shared
 // The pieces of one CTA's share of the units, in order.
 struct Pieces {
     const FlashParams &p;
-    long long u, end;
-    int i, h, pair, b0;
-    bool first;
-    // the current piece
+    int left, i, h, pair, b0;
+    // the current piece: blocks [cb0, cb1) of cnb; the share's first piece?
     int ci, ch, cpair, cb0, cb1, cnb;
     bool cfirst;
-    __device__ __forceinline__ Pieces(const FlashParams &p_, int cta) : p(p_), i(0), h(0), pair(0), first(true) {
-        const long long U = p.unit_off[p.nseq];
-        u = U * cta / p.ctas;
-        end = U * (cta + 1) / p.ctas;
-        if (u >= end) return;
-        while (u >= p.unit_off[i + 1]) ++i;
-        long long r = u - p.unit_off[i];
-        h = (int)(r / p.head_units[i]);
-        r %= p.head_units[i];
-        for (int nb; r >= (nb = flash_blocks(p.T[i], p.n[i], p.G, pair)); ++pair) r -= nb;
-        b0 = (int)r;
+    __device__ __forceinline__ Pieces(const FlashParams &p_, int cta) : p(p_), cfirst(false), cnb(0) {
+        const FlashParams::Share &s = p.share[cta];
+        left = s.units;
+        i = s.i; h = s.h; pair = s.pair; b0 = s.b0;
     }
     __device__ __forceinline__ bool next() {
-        if (u >= end) return false;
-        ci = i; ch = h; cpair = pair; cb0 = b0; cfirst = first;
+        if (left <= 0) return false;
+        cfirst = cnb == 0;
+        ci = i; ch = h; cpair = pair; cb0 = b0;
         cnb = flash_blocks(p.T[i], p.n[i], p.G, pair);
-        cb1 = (int)min((long long)cnb, b0 + (end - u));
-        u += cb1 - cb0;
-        first = false;
+        cb1 = min(cnb, b0 + left);
+        left -= cb1 - cb0;
         b0 = 0;
         if ((pair + 1) * FLASH_ROWS < p.n[i] * p.G) {
             ++pair;
@@ -54,8 +45,7 @@ struct Pieces {
             pair = 0;
             if (++h == p.H) {
                 h = 0;
-                do ++i;  // entries without units do not occur, but cost nothing here
-                while (i < p.nseq && p.unit_off[i + 1] == p.unit_off[i]);
+                ++i;
             }
         }
         return true;
@@ -93,6 +83,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // Two fp32 operations in one instruction.
@@ -133,7 +129,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 
 // ---------------------------------------------------------------- operand images
 
-// CTA (entry, head, block of 128 positions): the key and value images.  A
+// Item (entry, head, block of 128 positions; keys or values): one image.  A
 // factorized page's rows are L_K R_K and (transposed) R_V^T L_V^T, products of
 // the stored bf16 factors with fp32 sums (m16n8k16 on the warps: each product
 // is tiny and its operands lie as stored); dense rows and the chunk's come as
@@ -142,230 +138,291 @@ __device__ __forceinline__ float finite_abs(float x) {
 // and the scores' errors, unlike the output's rounding, grow with |s|.
 // (Rebuilt keys and values in bf16 left 6e-3 of the output's norm at 32K tokens,
 // 3.5 times the output's own rounding.)
+//
+// HBM-bound: 40 % of the image bytes are read, all are written.  Every step of
+// an item is short and waits on the one before, so CTAs stay and loop over
+// items: the next item's factors arrive and the last image leaves while one is
+// computed.
+struct StageItem {
+    int i, b, T0, T1, fw, h, blk, kv;
+    __device__ __forceinline__ StageItem(const StageParams &p, int item) {
+        kv = item & 1;
+        int u = item >> 1;
+        i = 0;
+        while (u >= p.blk_off[i + 1] * p.y.H) ++i;
+        const int nblk = p.blk_off[i + 1] - p.blk_off[i];
+        u -= p.blk_off[i] * p.y.H;
+        h = u / nblk;
+        blk = u - h * nblk;
+        b = p.seqs[i];
+        T0 = p.T[i];
+        T1 = T0 + p.n[i];
+        fw = p.fw[i];
+    }
+};
+
+// Bytes of a page's place in a fetch buffer: the larger factor part of a record,
+// or the page's dense rows.
+__host__ __device__ inline uint32_t stage_page_bytes(const Layout &y) {
+    const size_t kpart = y.off_LV, vpart = y.rec_bytes - y.off_LV, part = kpart > vpart ? kpart : vpart;
+    return (uint32_t)(part > y.dense_half_bytes ? part : y.dense_half_bytes);
+}
+constexpr int STAGE_THREADS = 512;
+
 template <int P, int D>
-__global__ void __launch_bounds__(256) stage_kernel(const StageParams p) {
+__global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StageParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
-    __shared__ uint64_t bar;
-    __shared__ float red[2][8];
+    __shared__ uint64_t bars[2];
+    __shared__ float red[STAGE_THREADS / 32];
     constexpr int NP = FLASH_KEYS / P, IMG = FLASH_KEYS * D * 2;
     const Layout &y = p.y;
-    unsigned char *imgK = sm, *imgV = sm + IMG, *recs = sm + 2 * IMG;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    int i = 0;
-    while ((int)blockIdx.x >= p.blk_off[i + 1] * y.H) ++i;
-    const int nblk = p.blk_off[i + 1] - p.blk_off[i];
-    const int u = (int)blockIdx.x - p.blk_off[i] * y.H, h = u / nblk, blk = u % nblk;
-    const int T0 = p.T[i], T1 = T0 + p.n[i], b = p.seqs[i];
-    auto factored = [&](int s) {
-        const int pg = blk * NP + s;
-        return pg * P < T0 && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
-    };
-    bool any = false;
-    for (int s = 0; s < NP; ++s) any |= factored(s);
-    if (any) {
-        if (tid == 0) {
-            mbar_init(&bar, 1);
-            fence_barrier_init();
-            uint32_t tx = 0;
-            for (int s = 0; s < NP; ++s) tx += factored(s) ? (uint32_t)y.rec_bytes : 0u;
-            mbar_arrive_expect_tx(&bar, tx);
-            for (int s = 0; s < NP; ++s)
-                if (factored(s))
-                    bulk_g2s(recs + s * y.rec_bytes, p.factor_pool + y.record_offset(p.layer, b, h, blk * NP + s),
-                             (uint32_t)y.rec_bytes, &bar);
-        }
-        __syncthreads();
-        const bool ok = __syncthreads_and(mbar_wait_bounded(&bar, 0, p.status) ? 1 : 0) != 0;
-        if (!ok) {  // let the copies land, then leave the images as they are
-            if (tid == 0) mbar_wait_bounded(&bar, 0, nullptr);
-            __syncthreads();
-            return;
-        }
-    }
-    const __nv_bfloat16 *knew = reinterpret_cast<const __nv_bfloat16 *>(p.k_new);
-    const __nv_bfloat16 *vnew = reinterpret_cast<const __nv_bfloat16 *>(p.v_new);
-
-    // keys: warp w holds positions 16w .. 16w + 15, all d columns
-    float acc[16][4];
-    {
-        const int s = 16 * warp / P, t0 = 16 * warp % P;
-#pragma unroll
-        for (int nt = 0; nt < D / 8; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-        if (factored(s)) {
-            const uint32_t LK = smem_u32(recs + s * y.rec_bytes), RK = LK + (uint32_t)y.off_RK;
-            const int pitch = y.rkp * 2;
-            int k0 = 0;
-            for (; k0 + 16 <= y.rkp; k0 += 16) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4(LK + swz_offset(t0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
-#pragma unroll
-                for (int nt = 0; nt < D / 8; nt += 2) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(RK + swz_offset(k0 + (lane & 15), 16 * nt + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
-                    mma16816(acc[nt], a0, a1, a2, a3, b0, b1);
-                    mma16816(acc[nt + 1], a0, a1, a2, a3, b2, b3);
-                }
-            }
-            if (k0 < y.rkp) {  // eight ranks left
-                uint32_t a0, a1;
-                ldsm_x2(LK + swz_offset(t0 + (lane & 15), 2 * k0, pitch), a0, a1);
-#pragma unroll
-                for (int nt = 0; nt < D / 8; nt += 4) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(RK + swz_offset(k0 + (lane & 7), 16 * nt + 16 * (lane >> 3), D * 2), b0, b1, b2, b3);
-                    mma1688(acc[nt], a0, a1, b0);
-                    mma1688(acc[nt + 1], a0, a1, b1);
-                    mma1688(acc[nt + 2], a0, a1, b2);
-                    mma1688(acc[nt + 3], a0, a1, b3);
-                }
-            }
-        } else {
-            const int pg = blk * NP + s;
-            const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, 0);
-#pragma unroll
-            for (int r2 = 0; r2 < 2; ++r2) {
-                const int t = t0 + g + 8 * r2, pos = pg * P + t;
-                if (pos >= T1) continue;
-#pragma unroll
-                for (int nt = 0; nt < D / 8; ++nt) {
-                    const int col = 8 * nt + 2 * c;
-                    const __nv_bfloat16 *src = pos < T0 ? swz_ptr<__nv_bfloat16>(page, t, col, D)
-                                                        : knew + ((size_t)(p.off[i] + pos - T0) * y.H + h) * D + col;
-                    const uint32_t v = *reinterpret_cast<const uint32_t *>(src);
-                    acc[nt][2 * r2] = bf16_lo_to_f32(v);
-                    acc[nt][2 * r2 + 1] = bf16_hi_to_f32(v);
-                }
-            }
-        }
-        if (y.rope) {  // turn each pair of columns (j, j + d/2) by its position
-            const int pg = blk * NP + s;
-#pragma unroll
-            for (int r2 = 0; r2 < 2; ++r2) {
-                const int t = t0 + g + 8 * r2;
-                if (pg * P + t >= T1) continue;
-#pragma unroll
-                for (int nt = 0; nt < D / 16; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 8 * nt + 2 * c + e;
-                        const float2 a = p.rope_base[(size_t)pg * (D / 2) + j], o = p.rope_delta[t * (D / 2) + j];
-                        const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
-                        float &x0 = acc[nt][2 * r2 + e], &x1 = acc[nt + D / 16][2 * r2 + e];
-                        const float u0 = x0 * cs - x1 * sn, u1 = x1 * cs + x0 * sn;
-                        x0 = u0;
-                        x1 = u1;
-                    }
-            }
-        }
-    }
-    auto block_max = [&](int which, int tiles) {
-        float m = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 16; ++nt)
-            if (nt < tiles)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m = fmaxf(m, finite_abs(acc[nt][e]));
-        m = warp_max(m);
-        if (lane == 0) red[which][warp] = m;
-        __syncthreads();
-        m = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[which][w]);
-        return m;
-    };
-    const int ek = fp16_exponent(block_max(0, D / 8));
-    {
-        const float f = pow2i(-ek);
-#pragma unroll
-        for (int nt = 0; nt < D / 8; ++nt)
-#pragma unroll
-            for (int r2 = 0; r2 < 2; ++r2) {
-                const int r = 16 * warp + g + 8 * r2;
-                *reinterpret_cast<uint32_t *>(imgK + (nt / 8) * (FLASH_KEYS * 128) + r * 128 + (((nt & 7) ^ (r & 7)) << 4) +
-                                              4 * c) = pack_f16(acc[nt][2 * r2] * f, acc[nt][2 * r2 + 1] * f);
-            }
-    }
-
-    // values, transposed: 16 head dimensions per warp; all 128 positions at D =
-    // 128, one half of them at D = 64
-    constexpr int VT = D == 128 ? 16 : 8;
-    const int d0 = 16 * (warp % (D / 16)), key0 = D == 128 ? 0 : 64 * (warp / 4);
-#pragma unroll
-    for (int nt = 0; nt < VT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-#pragma unroll
-    for (int s2 = 0; s2 < 8 * VT / P; ++s2) {
-        const int s = key0 / P + s2;
-        constexpr int PT = P / 8;  // position tiles of a page
-        if (factored(s)) {
-            const uint32_t LV = smem_u32(recs + s * y.rec_bytes) + (uint32_t)y.off_LV;
-            const uint32_t RV = smem_u32(recs + s * y.rec_bytes) + (uint32_t)y.off_RV;
-            const int pitch = y.rvp * 2;
-            int k0 = 0;
-            for (; k0 + 16 <= y.rvp; k0 += 16) {
-                uint32_t a0, a1, a2, a3;
-                ldsm_x4(RV + swz_offset(d0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
-#pragma unroll
-                for (int nt = 0; nt < PT; nt += 2) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4_t(LV + swz_offset(k0 + (lane & 15), 16 * nt + 16 * (lane >> 4), P * 2), b0, b1, b2, b3);
-                    mma16816(acc[s2 * PT + nt], a0, a1, a2, a3, b0, b1);
-                    mma16816(acc[s2 * PT + nt + 1], a0, a1, a2, a3, b2, b3);
-                }
-            }
-            if (k0 < y.rvp) {
-                uint32_t a0, a1;
-                ldsm_x2(RV + swz_offset(d0 + (lane & 15), 2 * k0, pitch), a0, a1);
-#pragma unroll
-                for (int nt = 0; nt < PT; nt += 2) {
-                    uint32_t b0, b1;
-                    const int row = k0 + (lane & 7), col = 16 * nt + 16 * ((lane >> 3) & 1);
-                    uint32_t addr = LV + swz_offset(row, col, P * 2);
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                                 : "=r"(b0), "=r"(b1) : "r"(addr));
-                    mma1688(acc[s2 * PT + nt], a0, a1, b0);
-                    mma1688(acc[s2 * PT + nt + 1], a0, a1, b1);
-                }
-            }
-        } else {
-            const int pg = blk * NP + s;
-            const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, 1);
-#pragma unroll
-            for (int nt = 0; nt < PT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int t = 8 * nt + 2 * c + (e & 1), pos = pg * P + t, dim = d0 + g + 8 * (e >> 1);
-                    if (pos >= T1) continue;
-                    const __nv_bfloat16 *src = pos < T0 ? swz_ptr<__nv_bfloat16>(page, t, dim, D)
-                                                        : vnew + ((size_t)(p.off[i] + pos - T0) * y.H + h) * D + dim;
-                    acc[s2 * PT + nt][e] = __bfloat162float(*src);
-                }
-        }
-    }
-    // values of ordinary size keep scale 1, so that a sequence's blocks agree
-    const float vmax = block_max(1, VT);
-    const int ev = vmax > 0.f && (vmax >= 32768.f || vmax < 0.00390625f) ? fp16_exponent(vmax) : 0;
-    {
-        const float f = pow2i(-ev);
-#pragma unroll
-        for (int nt = 0; nt < VT; ++nt)
-#pragma unroll
-            for (int r2 = 0; r2 < 2; ++r2) {
-                const int r = d0 + g + 8 * r2, key = key0 + 8 * nt;
-                *reinterpret_cast<uint32_t *>(imgV + (key / 64) * (D * 128) + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4) +
-                                              4 * c) = pack_f16(acc[nt][2 * r2] * f, acc[nt][2 * r2 + 1] * f);
-            }
-    }
-    fence_proxy_async_shared();
-    __syncthreads();
+    const int items = 2 * p.blk_off[p.nseq] * y.H;
+    const uint32_t kpart = (uint32_t)y.off_LV, vpart = (uint32_t)(y.rec_bytes - y.off_LV);  // each one stretch of a record
+    const uint32_t page_bytes = stage_page_bytes(y);
+    unsigned char *img = sm;
     if (tid == 0) {
-        char *dst = p.images + (size_t)blockIdx.x * (2 * IMG);
-        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(imgK)),
-                     "r"((uint32_t)(2 * IMG))
-                     : "memory");
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        p.scales[blockIdx.x] = make_float2((float)ek, (float)ev);
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        fence_barrier_init();
     }
+    __syncthreads();
+    // factorized pages of an item: [first, last) of its NP pages
+    auto first = [&](const StageItem &it) { return max(0, min(NP, y.sink_pages - it.blk * NP)); };
+    auto last = [&](const StageItem &it) { return max(0, min(NP, it.fw - it.blk * NP)); };
+    auto fetch = [&](int item, int buf) {  // thread 0: the factors of an item
+        const StageItem it(p, item);
+        const int s0 = first(it), s1 = last(it);
+        if (s0 >= s1) return;
+        const uint32_t part = it.kv ? vpart : kpart;
+        mbar_arrive_expect_tx(&bars[buf], (uint32_t)(s1 - s0) * part);
+        const char *src = p.factor_pool + y.record_offset(p.layer, it.b, it.h, it.blk * NP + s0) + (it.kv ? kpart : 0u);
+        for (int s = s0; s < s1; ++s, src += y.rec_bytes)
+            bulk_g2s(sm + IMG + (buf * NP + s) * page_bytes, src, part, &bars[buf]);
+    };
+    if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
+    uint32_t phase = 0;  // bit of each buffer's barrier
+    int buf = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
+        const int next = item + gridDim.x;
+        if (tid == 0 && next < items) fetch(next, buf ^ 1);
+        const StageItem it(p, item);
+        const int s_lo = first(it), s_hi = last(it), pg0 = it.blk * NP;
+        unsigned char *recs = sm + IMG + buf * NP * page_bytes;
+        // dense pages, the chunk's rows and zeros past the end, in the dense
+        // pages' swizzled rows
+        if (s_lo > 0 || s_hi < NP || s_lo >= s_hi) {
+            const char *chunk = it.kv ? p.v_new : p.k_new;
+            constexpr int CH = D / 8;  // 16-byte chunks of a row
+            constexpr int PER = FLASH_KEYS * CH / STAGE_THREADS;
+            uint4 v[PER];
+            int slot = -1;
+            const char *page = nullptr;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, s = row / P, pos = pg0 * P + row;
+                v[k] = make_uint4(0, 0, 0, 0);
+                if ((s >= s_lo && s < s_hi) || pos >= it.T1) continue;
+                if (pos >= it.T0) {
+                    v[k] = reinterpret_cast<const uint4 *>(chunk + ((size_t)(p.off[it.i] + pos - it.T0) * y.H + it.h) * (D * 2))[ch];
+                } else {
+                    if (s != slot) {
+                        slot = s;
+                        page = p.dense_pool + y.dense_offset(p.layer, it.b, y.dense_slot(pg0 + s), it.h, it.kv);
+                    }
+                    v[k] = *reinterpret_cast<const uint4 *>(page + swz_offset(row % P, 16 * ch, D * 2));
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, s = row / P;
+                if (s >= s_lo && s < s_hi) continue;
+                *reinterpret_cast<uint4 *>(recs + s * page_bytes + swz_offset(row % P, 16 * ch, D * 2)) = v[k];
+            }
+            __syncthreads();
+        }
+        if (s_lo < s_hi) {
+            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
+            if (!ok) {  // let the copies land, then leave the images as they are
+                if (tid == 0) {
+                    mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
+                    if (next < items) {
+                        const StageItem nx(p, next);
+                        if (first(nx) < last(nx)) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
+                    }
+                }
+                break;
+            }
+            phase ^= 1u << buf;
+        }
+        float acc[8][4];
+        // the largest finite |acc| of the CTA; also past the last image's store
+        auto block_max = [&](int tiles) {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < tiles)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m = fmaxf(m, finite_abs(acc[j][e]));
+            m = warp_max(m);
+            if (lane == 0) red[warp] = m;
+            if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncthreads();
+            m = lane < STAGE_THREADS / 32 ? red[lane] : 0.f;
+            return warp_max(m);
+        };
+        auto put = [&](uint32_t r0, uint32_t r1, float *d) {  // a bf16 pair of row g, and of row g + 8
+            d[0] = bf16_lo_to_f32(r0);
+            d[1] = bf16_hi_to_f32(r0);
+            d[2] = bf16_lo_to_f32(r1);
+            d[3] = bf16_hi_to_f32(r1);
+        };
+        int scale;  // the image's power of two
+        if (it.kv == 0) {
+            // warp: positions 16 w .. 16 w + 15 and half of the columns, tile j
+            // = columns 8 nt(j) .. + 7; column pairs that RoPE turns stay together
+            constexpr int KT = D / 16;
+            const int w = warp & 7, half = warp >> 3, s = 16 * w / P, t0 = 16 * w % P, pg = pg0 + s;
+            auto nt = [&](int j) { return j % (KT / 2) + KT / 2 * half + KT * (j / (KT / 2)); };
+#pragma unroll
+            for (int j = 0; j < KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            const uint32_t base = smem_u32(recs + s * page_bytes);
+            if (s >= s_lo && s < s_hi) {
+                const uint32_t RK = base + (uint32_t)y.off_RK;
+                const int pitch = y.rkp * 2;
+                int k0 = 0;
+                for (; k0 + 16 <= y.rkp; k0 += 16) {
+                    uint32_t a0, a1, a2, a3;
+                    ldsm_x4(base + swz_offset(t0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+#pragma unroll
+                    for (int j = 0; j < KT; j += 2) {
+                        uint32_t b0, b1, b2, b3;
+                        ldsm_x4_t(RK + swz_offset(k0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
+                        mma16816(acc[j], a0, a1, a2, a3, b0, b1);
+                        mma16816(acc[j + 1], a0, a1, a2, a3, b2, b3);
+                    }
+                }
+                if (k0 < y.rkp) {  // eight ranks left
+                    uint32_t a0, a1;
+                    ldsm_x2(base + swz_offset(t0 + (lane & 15), 2 * k0, pitch), a0, a1);
+#pragma unroll
+                    for (int j = 0; j < KT; j += 2) {
+                        uint32_t b0, b1;
+                        ldsm_x2_t(RK + swz_offset(k0 + (lane & 7), 16 * nt(j) + 16 * ((lane >> 3) & 1), D * 2), b0, b1);
+                        mma1688(acc[j], a0, a1, b0);
+                        mma1688(acc[j + 1], a0, a1, b1);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < KT; j += 2) {
+                    uint32_t r0, r1, r2, r3;
+                    ldsm_x4(base + swz_offset(t0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), r0, r1, r2, r3);
+                    put(r0, r1, acc[j]);
+                    put(r2, r3, acc[j + 1]);
+                }
+            }
+            if (y.rope) {  // turn each pair of columns (i, i + d/2) by its position
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2) {
+                    const int t = t0 + g + 8 * r2;
+                    if (pg * P + t >= it.T1) continue;
+#pragma unroll
+                    for (int j = 0; j < KT / 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int i = 8 * nt(j) + 2 * c + e;
+                            const float2 a = p.rope_base[(size_t)pg * (D / 2) + i], o = p.rope_delta[t * (D / 2) + i];
+                            const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
+                            float &x0 = acc[j][2 * r2 + e], &x1 = acc[j + KT / 2][2 * r2 + e];
+                            const float u0 = x0 * cs - x1 * sn, u1 = x1 * cs + x0 * sn;
+                            x0 = u0;
+                            x1 = u1;
+                        }
+                }
+            }
+            scale = fp16_exponent(block_max(KT));
+            const float f = pow2i(-scale);
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2) {
+                    const int r = 16 * w + g + 8 * r2;
+                    *reinterpret_cast<uint32_t *>(img + (nt(j) / 8) * (FLASH_KEYS * 128) + r * 128 +
+                                                  (((nt(j) & 7) ^ (r & 7)) << 4) + 4 * c) =
+                        pack_f16(acc[j][2 * r2] * f, acc[j][2 * r2 + 1] * f);
+                }
+        } else {
+            // transposed; warp: 16 head dimensions, KR positions
+            constexpr int KR = D == 128 ? 64 : 32, PK = P < KR ? P : KR, PT = PK / 8;
+            const int d0 = 16 * (warp % (D / 16)), key0 = KR * (warp / (D / 16));
+#pragma unroll
+            for (int j = 0; j < KR / 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+            for (int s2 = 0; s2 < KR / PK; ++s2) {
+                const int s = (key0 + s2 * PK) / P, off = (key0 + s2 * PK) % P;  // page, its first position here
+                const uint32_t base = smem_u32(recs + s * page_bytes);
+                if (s >= s_lo && s < s_hi) {
+                    const uint32_t RV = base + (uint32_t)(y.off_RV - y.off_LV);
+                    const int pitch = y.rvp * 2;
+                    int k0 = 0;
+                    for (; k0 + 16 <= y.rvp; k0 += 16) {
+                        uint32_t a0, a1, a2, a3;
+                        ldsm_x4(RV + swz_offset(d0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+#pragma unroll
+                        for (int j = 0; j < PT; j += 2) {
+                            uint32_t b0, b1, b2, b3;
+                            ldsm_x4_t(base + swz_offset(k0 + (lane & 15), 2 * off + 16 * j + 16 * (lane >> 4), P * 2), b0, b1, b2, b3);
+                            mma16816(acc[s2 * PT + j], a0, a1, a2, a3, b0, b1);
+                            mma16816(acc[s2 * PT + j + 1], a0, a1, a2, a3, b2, b3);
+                        }
+                    }
+                    if (k0 < y.rvp) {
+                        uint32_t a0, a1;
+                        ldsm_x2(RV + swz_offset(d0 + (lane & 15), 2 * k0, pitch), a0, a1);
+#pragma unroll
+                        for (int j = 0; j < PT; j += 2) {
+                            uint32_t b0, b1;
+                            ldsm_x2_t(base + swz_offset(k0 + (lane & 7), 2 * off + 16 * j + 16 * ((lane >> 3) & 1), P * 2), b0, b1);
+                            mma1688(acc[s2 * PT + j], a0, a1, b0);
+                            mma1688(acc[s2 * PT + j + 1], a0, a1, b1);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < PT; j += 2) {
+                        uint32_t r0, r1, r2, r3;
+                        ldsm_x4_t(base + swz_offset(off + 8 * j + (lane & 7) + 8 * (lane >> 4), 2 * d0 + 16 * ((lane >> 3) & 1), D * 2),
+                                  r0, r1, r2, r3);
+                        put(r0, r1, acc[s2 * PT + j]);
+                        put(r2, r3, acc[s2 * PT + j + 1]);
+                    }
+                }
+            }
+            // values of ordinary size keep scale 1, so that a sequence's blocks agree
+            const float vmax = block_max(KR / 8);
+            scale = vmax > 0.f && (vmax >= 32768.f || vmax < 0.00390625f) ? fp16_exponent(vmax) : 0;
+            const float f = pow2i(-scale);
+#pragma unroll
+            for (int j = 0; j < KR / 8; ++j)
+#pragma unroll
+                for (int r2 = 0; r2 < 2; ++r2) {
+                    const int r = d0 + g + 8 * r2, key = key0 + 8 * j;
+                    *reinterpret_cast<uint32_t *>(img + (key / 64) * (D * 128) + r * 128 + ((((key & 63) >> 3) ^ (r & 7)) << 4) +
+                                                  4 * c) = pack_f16(acc[j][2 * r2] * f, acc[j][2 * r2 + 1] * f);
+                }
+        }
+        fence_proxy_async_shared();  // the image is written, the fetch buffer is read
+        __syncthreads();
+        if (tid == 0) {
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(p.images + (size_t)item * IMG),
+                         "r"(smem_u32(img)), "r"((uint32_t)IMG)
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            reinterpret_cast<float *>(p.scales)[item] = (float)scale;
+        }
+    }
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- attention
@@ -481,16 +538,16 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 {  // eight short chains of three-input maxima
                     float a[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) a[e] = __uint_as_float(x[0][e]);
+                    for (int j = 0; j < 8; ++j) a[j] = __uint_as_float(x[0][j]);
 #pragma unroll
-                    for (int e = 8; e < 128; e += 16)
+                    for (int e = 8; e < 120; e += 16)
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float v0 = __uint_as_float(x[(e + j) / 32][(e + j) & 31]);
-                            const float v1 = e + 8 + j < 128 ? __uint_as_float(x[((e + 8 + j) / 32) & 3][(e + 8 + j) & 31]) : v0;
-                            a[j] = fmaxf(fmaxf(a[j], v0), v1);
-                        }
-                    mx = fmaxf(fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])), fmaxf(fmaxf(a[4], a[5]), fmaxf(a[6], a[7])));
+                        for (int j = 0; j < 8; ++j)
+                            a[j] = max3(a[j], __uint_as_float(x[(e + j) / 32][(e + j) & 31]),
+                                        __uint_as_float(x[(e + 8 + j) / 32][(e + 8 + j) & 31]));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a[j] = fmaxf(a[j], __uint_as_float(x[3][24 + j]));
+                    mx = fmaxf(max3(max3(a[0], a[1], a[2]), a[3], a[4]), max3(a[5], a[6], a[7]));
                 }
                 mx *= cf;
                 // The reference m moves only when a score exceeds it by 2^8 (the
@@ -681,74 +738,87 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
     if (warp == 0) tmem_free(tmem, 512);
 }
 
-// Join the states of pairs cut between CTAs, eq. (5): block (pair, group of 32
-// rows), one warp per row, pieces in order (the same sums in every launch).
+// Join the states of the pairs cut between CTAs, eq. (5).  Block (boundary,
+// group of 32 rows): the boundary of shares c and c + 1, if it cuts a pair and is
+// the first that does; one warp per row, the pieces' o summed in order, the same in
+// every launch.
 template <int D>
 __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the pair, by its number over all entries
-    int i = 0, u = blockIdx.x;
-    for (; i < p.nseq; ++i) {
-        const int here = (p.n[i] * p.G + FLASH_ROWS - 1) / FLASH_ROWS * p.H;
-        if (u < here) break;
-        u -= here;
-    }
-    const int R = p.n[i] * p.G, pairs = (R + FLASH_ROWS - 1) / FLASH_ROWS, h = u / pairs, pair = u % pairs;
-    long long u0 = p.unit_off[i] + h * p.head_units[i];
-    for (int k = 0; k < pair; ++k) u0 += flash_blocks(p.T[i], p.n[i], p.G, k);
-    const long long u1 = u0 + flash_blocks(p.T[i], p.n[i], p.G, pair), U = p.unit_off[p.nseq];
-    auto owner = [&](long long x) {  // the CTA whose share [U c / ctas, U (c + 1) / ctas) holds unit x
-        int c = (int)(x * p.ctas / U);
-        while (U * (c + 1) / p.ctas <= x) ++c;
-        while (U * c / p.ctas > x) --c;
-        return c;
-    };
-    const int c0 = owner(u0), c1 = owner(u1 - 1);
-    if (c0 == c1) return;
-    const int slot0 = U * c0 / p.ctas == u0 ? 2 * c0 : 2 * c0 + 1;
+    const FlashParams::Share &cut = p.share[blockIdx.x + 1], &before = p.share[blockIdx.x];
+    // units from the pair's first on: cut.b0 before the boundary
+    if (cut.b0 == 0 || before.units < cut.b0) return;
+    const int i = cut.i, h = cut.h, pr = cut.pair;
+    const int nb = flash_blocks(p.T[i], p.n[i], p.G, pr);
+    const int c0 = blockIdx.x;  // the CTA that begins the pair
+    int c1 = c0 + 1;            // and the one that ends it
+    for (int at = cut.b0 + cut.units; at < nb; at += p.share[c1].units) ++c1;
+    const int np = c1 - c0 + 1, slot0 = before.units == cut.b0 ? 2 * c0 : 2 * c0 + 1;
+    const int R = p.n[i] * p.G;
     constexpr int V = D / 32;
-    for (int k = warp; k < 32; k += 8) {
-        const int rr = 32 * blockIdx.y + k, r = pair * FLASH_ROWS + rr;
-        if (r >= R) break;
-        auto row = [&](int c) { return p.partials + ((size_t)(c == c0 ? slot0 : 2 * c) * FLASH_ROWS + rr) * (D + 4); };
-        float M = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, row(c)[0]);
+    {
+        const int rr = 8 * blockIdx.y + warp, r = pr * FLASH_ROWS + rr;
+        if (r >= R) return;
+        auto row = [&](int c) { return p.partials + ((size_t)(c == 0 ? slot0 : 2 * (c0 + c)) * FLASH_ROWS + rr) * (D + 4); };
+        // the first 32 (m, l) and the first eight o come in one trip to memory
+        float2 ml = lane < np ? *reinterpret_cast<const float2 *>(row(lane)) : make_float2(-INFINITY, 0.f);
+        float o[8][V];
+        auto fetch = [&](int c0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[j][e] = c0 + j < np ? row(c0 + j)[4 + lane * V + e] : 0.f;
+        };
+        fetch(0);
+        float M = ml.x;
+        for (int c = lane + 32; c < np; c += 32) M = fmaxf(M, row(c)[0]);
         M = warp_max(M);
         float L = 0.f, acc[V] = {};
-        for (int c = c0; c <= c1; ++c) {
-            const float *q = row(c);
-            const float f = ex2(q[0] - M);
-            L = fmaf(f, q[1], L);
+        for (int cb = 0; cb < np; cb += 32) {
+            if (cb) ml = cb + lane < np ? *reinterpret_cast<const float2 *>(row(cb + lane)) : make_float2(-INFINITY, 0.f);
+            const float f = ex2(ml.x - M);
+            L = fmaf(f, ml.y, L);
+            for (int c = 0; c < 32 && cb + c < np; c += 8) {
+                if (cb + c) fetch(cb + c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] = fmaf(f, q[4 + lane * V + j], acc[j]);
+                for (int j = 0; j < 8; ++j) {
+                    const float fj = __shfl_sync(0xffffffffu, f, c + j);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(fj, o[j][e], acc[e]);
+                }
+            }
         }
-        const float il = 1.f / L;
+        const float il = 1.f / warp_sum(L);
         __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) +
                              ((size_t)(p.off[i] + r / p.G) * p.Hq + h * p.G + r % p.G) * D;
 #pragma unroll
-        for (int j = 0; j < V; ++j) dst[lane * V + j] = __float2bfloat16_rn(acc[j] * il);
+        for (int e = 0; e < V; ++e) dst[lane * V + e] = __float2bfloat16_rn(acc[e] * il);
     }
 }
 
 template <int P, int D>
-static cudaError_t stage_t(const StageParams &p, cudaStream_t st) {
-    const int smem = 2 * FLASH_KEYS * D * 2 + FLASH_KEYS / P * (int)p.y.rec_bytes;
-    cudaError_t e = cudaFuncSetAttribute(stage_kernel<P, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+static cudaError_t stage_t(const StageParams &p, int num_sms, cudaStream_t st) {
+    const int smem = FLASH_KEYS * D * 2 + 2 * FLASH_KEYS / P * (int)stage_page_bytes(p.y);  // at most 32 + 2 x 41 KB
+    auto k = stage_kernel<P, D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
-    stage_kernel<P, D><<<(unsigned)(p.blk_off[p.nseq] * p.y.H), 256, smem, st>>>(p);
+    const int items = 2 * p.blk_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
+    k<<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_stage(const StageParams &p, cudaStream_t st) {
+cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st) {
     if (p.blk_off[p.nseq] == 0) return cudaSuccess;
     if (p.y.d == 64) {
-        if (p.y.P == 16) return stage_t<16, 64>(p, st);
-        if (p.y.P == 32) return stage_t<32, 64>(p, st);
-        return stage_t<64, 64>(p, st);
+        if (p.y.P == 16) return stage_t<16, 64>(p, num_sms, st);
+        if (p.y.P == 32) return stage_t<32, 64>(p, num_sms, st);
+        return stage_t<64, 64>(p, num_sms, st);
     }
-    if (p.y.P == 16) return stage_t<16, 128>(p, st);
-    if (p.y.P == 32) return stage_t<32, 128>(p, st);
-    return stage_t<64, 128>(p, st);
+    if (p.y.P == 16) return stage_t<16, 128>(p, num_sms, st);
+    if (p.y.P == 32) return stage_t<32, 128>(p, num_sms, st);
+    return stage_t<64, 128>(p, num_sms, st);
 }
 
 template <int D>
@@ -759,17 +829,14 @@ static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
     flash_kernel<D><<<(unsigned)p.ctas, FLASH_THREADS, smem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.ctas == 1) return e;
-    int pairs = 0, most = 0;
-    for (int i = 0; i < p.nseq; ++i) {
-        pairs += (p.n[i] * p.G + FLASH_ROWS - 1) / FLASH_ROWS * p.H;
-        most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
-    }
-    flash_merge_kernel<D><<<dim3((unsigned)pairs, (unsigned)((most + 31) / 32)), 256, 0, st>>>(p);
+    int most = 0;
+    for (int i = 0; i < p.nseq; ++i) most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
+    flash_merge_kernel<D><<<dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st) {
-    if (p.unit_off[p.nseq] == 0) return cudaSuccess;
+    if (p.units == 0) return cudaSuccess;
     return d == 64 ? flash_t<64>(p, st) : flash_t<128>(p, st);
 }
 

@@ -190,6 +190,8 @@ struct ChunkAttnParams {
     int tile_off[MAX_CALL_BATCH + 1];  // CTAs of the entries before (filled by the launcher)
 };
 
+constexpr int FLASH_ROWS = 256, FLASH_KEYS = 128;  // query rows of a pair of tiles, keys of a block
+
 // Chunk attention on the fifth-generation tensor cores (bf16 stores).  The
 // entries' rows 0 .. T + n - 1 are laid out as fp16 operand images, one pair
 // (keys [128][d], values transposed [d][128], both K-major in the 128-byte
@@ -206,6 +208,7 @@ struct StageParams {
     int *status;
     int layer, nseq;
     int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH];
+    int fw[MAX_CALL_BATCH];  // page after the last factorized one (pages [sink_pages, fw) are)
     int blk_off[MAX_CALL_BATCH + 1];
 };
 
@@ -213,6 +216,7 @@ struct StageParams {
 // p attends blocks 0 .. flash_blocks() - 1.  All (entry, head, pair, block)
 // units in this order are shared out evenly over ctas CTAs; the states of
 // pairs cut between CTAs go to partials ([2 ctas][256][d + 4]).
+constexpr int FLASH_MAX_CTAS = 256;
 struct FlashParams {
     int H, Hq, G, nseq, ctas;
     float scale_log2;
@@ -223,9 +227,12 @@ struct FlashParams {
     float *partials;
     int *status;
     int T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH], blk_off[MAX_CALL_BATCH + 1];
-    long long head_units[MAX_CALL_BATCH], unit_off[MAX_CALL_BATCH + 1];
+    long long units;  // of all entries
+    // share of CTA c: units[c] units from block b0 of (entry, head, pair) on
+    struct Share {
+        int i, h, pair, b0, units;
+    } share[FLASH_MAX_CTAS];
 };
-constexpr int FLASH_ROWS = 256, FLASH_KEYS = 128;  // query rows of a pair of tiles, keys of a block
 
 // Blocks that pair p of an entry of T cached and n new tokens attends.
 PKV_HD int flash_blocks(int T, int n, int G, int p) {
@@ -233,7 +240,7 @@ PKV_HD int flash_blocks(int T, int n, int G, int p) {
     return (T + (last - 1) / G) / FLASH_KEYS + 1;
 }
 
-cudaError_t launch_stage(const StageParams &p, cudaStream_t st);
+cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st);
 
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st);
