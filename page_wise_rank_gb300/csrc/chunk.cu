@@ -151,18 +151,36 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkAttnParams 
     const int u = (int)(w - p.tile_off[i]), h = u / R, r = u % R;
     const float *rows = p.partials + (size_t)(p.poff[i] + (long long)h * ns * R + r) * (D + 4);
     const size_t pitch = (size_t)R * (D + 4);
-    float M = -INFINITY;
-    for (int s = lane; s < ns; s += 32) M = fmaxf(M, rows[s * pitch]);
-    M = warp_max(M);
     constexpr int V = D / 32;
-    float L = 0.f, acc[V] = {};
-    for (int s = 0; s < ns; ++s) {
-        const float *row = rows + s * pitch;
-        const float c = exp2f(row[0] - M);
-        L = fmaf(c, row[1], L);
+    // the first 32 (m, l) and the first eight o come in one trip to memory
+    float2 ml = lane < ns ? *reinterpret_cast<const float2 *>(rows + lane * pitch) : make_float2(-INFINITY, 0.f);
+    float o[8][V];
+    auto fetch = [&](int s0) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(c, row[4 + lane * V + k], acc[k]);
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[j][k] = s0 + j < ns ? rows[(s0 + j) * pitch + 4 + lane * V + k] : 0.f;
+    };
+    fetch(0);
+    float M = ml.x;
+    for (int s = lane + 32; s < ns; s += 32) M = fmaxf(M, rows[s * pitch]);
+    M = warp_max(M);
+    float L = 0.f, acc[V] = {};
+    for (int sb = 0; sb < ns; sb += 32) {
+        if (sb) ml = sb + lane < ns ? *reinterpret_cast<const float2 *>(rows + (sb + lane) * pitch) : make_float2(-INFINITY, 0.f);
+        const float f = exp2f(ml.x - M);
+        L = fmaf(f, ml.y, L);
+        for (int s = 0; s < 32 && sb + s < ns; s += 8) {
+            if (sb + s) fetch(sb + s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float fj = __shfl_sync(0xffffffffu, f, s + j);
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] = fmaf(fj, o[j][k], acc[k]);
+            }
+        }
     }
+    L = warp_sum(L);
     const float il = 1.f / L;
     T *dst = reinterpret_cast<T *>(p.out) + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D;
 #pragma unroll

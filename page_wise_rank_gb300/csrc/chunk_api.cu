@@ -82,98 +82,190 @@ int first_window_page(const Layout &y, int T) {
     return fw;
 }
 
-// What a chunk attention call places in its workspace.
+// What a chunk attention call runs and places in its workspace.
 struct AttnPlan {
-    ChunkAttnParams a{};  // fp32 and INT4 stores
-    FlashParams f{};      // other bf16 stores
-    bool flash = false;
-    int seq[MAX_CALL_BATCH];
-    long long rows = 0;  // dense key / value rows of the listed sequences
-    size_t v_off = 0, scale_off = 0, part_off = 0, bytes = 0;
+    int nseq = 0;                      // entries with new tokens, and their cached lengths
+    int seqs[MAX_CALL_BATCH], lens[MAX_CALL_BATCH];
+    SmallParams s{};                   // bf16 stores: entries of few query rows
+    FlashParams f{};                   // bf16 stores: the others (staged as `g`)
+    StageParams g{};
+    ChunkAttnParams a{};               // fp32 and INT4 stores, rebuilt by `r`; the merge of split states
+    RowsParams r{};
+    size_t images = 0, scales = 0, flash_parts = 0, keys = 0, values = 0, parts = 0, bytes = 0;  // offsets, total
 };
 
-// The tensor-core path: operand images, their scales, the cut pairs' states.
-void plan_flash(const puzzlekv_store *s, AttnPlan &pl) {
+void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
+    rp = RowsParams{};
+    rp.y = s->y;
+    rp.factor_pool = s->factor_pool;
+    rp.dense_pool = s->dense_pool;
+    rp.rope_base = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_base_offset);
+    rp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_delta_offset);
+    rp.layer = layer;
+    rp.turn = 1;
+}
+
+// Splits of the few-token path's entries over the SMs (one CTA each): every KV
+// head's CTAs go to the entries in proportion to the bytes they stream.  One
+// wave of CTAs is best when the shares come out even; lists of unequal lengths
+// fill the SMs better with up to four.  A CTA's start and merge cost about as
+// much as streaming 110 KB.
+void split_small(const puzzlekv_store *s, SmallParams &p) {
     const Layout &y = s->y;
-    const ChunkAttnParams &a = pl.a;
-    FlashParams &f = pl.f;
-    f.H = a.H; f.Hq = a.Hq; f.G = a.G;
-    f.scale_log2 = a.scale_log2;
-    f.nseq = a.nseq;
-    for (int j = 0; j < a.nseq; ++j) {
-        f.T[j] = a.T[j];
-        f.n[j] = a.n[j];
-        f.off[j] = a.off[j];
-        f.blk_off[j + 1] = f.blk_off[j] + (a.T[j] + a.n[j] + FLASH_KEYS - 1) / FLASH_KEYS;
+    constexpr double kCta = 110e3;
+    const long long rec = (long long)y.rec_bytes, half = (long long)y.P * y.d * y.esz;
+    std::vector<double> cost(p.nseq);
+    double total = 0, best = 0;
+    for (int i = 0; i < p.nseq; ++i) {
+        const PageSplit ps(p.T[i], y.P, y.sink_pages, y.sink_tokens, y.W, rec, half, 1);
+        cost[i] = (double)ps.total + (double)p.n[i] * y.d * 2 * y.esz;
+        total += cost[i];
     }
+    std::vector<int> ns(p.nseq), pick(p.nseq, 1);
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int want = std::min(700, std::max(1, s->num_sms * waves / y.H));
+        double most = 0;
+        int ctas = 0;
+        for (int i = 0; i < p.nseq; ++i) {
+            const int pages = (p.T[i] + y.P - 1) / y.P;
+            ns[i] = std::max(1, std::min({pages, MAX_SPLITS, (int)std::lround(cost[i] * want / total)}));
+            most = std::max(most, cost[i] / ns[i]);
+            ctas += ns[i] * y.H;
+        }
+        const int rounds = (ctas + s->num_sms - 1) / s->num_sms;
+        const double t = std::max(most + kCta, total * y.H / s->num_sms) + kCta * rounds + (rounds - 1) * most / 2;
+        if (waves == 1 || t < best) {
+            best = t;
+            pick = ns;
+        }
+    }
+    for (int i = 0; i < p.nseq; ++i) {
+        p.ns[i] = pick[i];
+        const PageSplit ps(p.T[i], y.P, y.sink_pages, y.sink_tokens, y.W, rec, half, p.ns[i]);
+        for (int r = 0; r <= p.ns[i]; ++r) p.bounds[p.boff[i] + r] = ps.begin(r);
+        p.boff[i + 1] = p.boff[i] + p.ns[i] + 1;
+    }
+}
+
+// The shares of the tensor-memory path's CTAs.
+void split_flash(const puzzlekv_store *s, FlashParams &f) {
     // units before each pair of every entry, one head
-    std::vector<std::vector<long long>> before(a.nseq);
+    std::vector<std::vector<long long>> before(f.nseq);
     std::vector<long long> head_off;  // units before (entry, head), in order
     long long U = 0;
-    for (int j = 0; j < a.nseq; ++j) {
+    for (int j = 0; j < f.nseq; ++j) {
         std::vector<long long> &u = before[j];
         u.push_back(0);
-        for (int p = 0; (long long)p * FLASH_ROWS < (long long)a.n[j] * a.G; ++p)
-            u.push_back(u.back() + flash_blocks(a.T[j], a.n[j], a.G, p));
-        for (int h = 0; h < a.H; ++h, U += u.back()) head_off.push_back(U);
+        for (int p = 0; (long long)p * FLASH_ROWS < (long long)f.n[j] * f.G; ++p)
+            u.push_back(u.back() + flash_blocks(f.T[j], f.n[j], f.G, p));
+        for (int h = 0; h < f.H; ++h, U += u.back()) head_off.push_back(U);
     }
     f.units = U;
-    f.ctas = (int)std::min<long long>(std::min(s->num_sms, FLASH_MAX_CTAS), std::max(1LL, U));
+    f.ctas = (int)std::min<long long>(std::min(s->num_sms, FLASH_MAX_CTAS), U);
     for (int c = 0; c < f.ctas; ++c) {
         const long long u0 = U * c / f.ctas, u1 = U * (c + 1) / f.ctas;
         const int eh = (int)(std::upper_bound(head_off.begin(), head_off.end(), u0) - head_off.begin()) - 1;
-        const std::vector<long long> &u = before[eh / a.H];
+        const std::vector<long long> &u = before[eh / f.H];
         const long long r = u0 - head_off[eh];
         const int pair = (int)(std::upper_bound(u.begin(), u.end(), r) - u.begin()) - 1;
-        f.share[c] = {eh / a.H, eh % a.H, pair, (int)(r - u[pair]), (int)(u1 - u0)};
+        f.share[c] = {eh / f.H, eh % f.H, pair, (int)(r - u[pair]), (int)(u1 - u0)};
     }
-    const size_t blocks = (size_t)f.blk_off[f.nseq] * y.H;
-    pl.scale_off = blocks * (2 * FLASH_KEYS * y.d * 2);
-    pl.part_off = pl.scale_off + up256(blocks * sizeof(float2));
-    pl.bytes = pl.part_off + (f.ctas > 1 ? (size_t)2 * f.ctas * FLASH_ROWS * (y.d + 4) * 4 : 0);
 }
 
 void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *counts, int32_t B,
                     AttnPlan &pl) {
     const Layout &y = s->y;
+    const float scale = (float)(1.4426950408889634074 / std::sqrt((double)y.d));
+    const bool tensor = y.dtype == 1 && !y.q4;
+    int most_small = 0;
+    if (tensor && !y.rope)
+        for (int i = 0; i < B; ++i)
+            if (counts[i] <= SMALL_ROWS / y.G) most_small = std::max(most_small, counts[i]);
+    const int small_tokens = most_small && small_smem_bytes(y, most_small) ? most_small : 0;
     ChunkAttnParams &a = pl.a;
     a.H = y.H; a.Hq = y.Hq; a.G = y.G; a.d = y.d;
-    a.scale_log2 = (float)(1.4426950408889634074 / std::sqrt((double)y.d));
+    a.scale_log2 = scale;
+    pl.s.y = y;
+    pl.s.scale_log2 = scale;
+    pl.s.layer = layer;
+    FlashParams &f = pl.f;
+    f.H = y.H; f.Hq = y.Hq; f.G = y.G;
+    f.scale_log2 = scale;
+    rows_params(s, layer, pl.r);
+    StageParams &g = pl.g;
+    g.y = y;
+    g.factor_pool = s->factor_pool;
+    g.dense_pool = s->dense_pool;
+    g.rope_base = pl.r.rope_base;
+    g.rope_delta = pl.r.rope_delta;
+    g.layer = layer;
     long tiles = 0;
+    long long rows = 0, parts = 0;
     int off = 0;
-    for (int i = 0; i < B; ++i) {
-        const int n = counts[i], T = length_of(s, seq_ids[i], layer);
-        const int j = a.nseq;
-        if (n > 0) {
-            pl.seq[j] = seq_ids[i];
-            a.T[j] = T;
-            a.n[j] = n;
-            a.off[j] = off;
-            a.koff[j] = pl.rows;
-            pl.rows += T + n;
+    for (int i = 0; i < B; off += counts[i], ++i) {
+        const int n = counts[i], T = length_of(s, seq_ids[i], layer), fw = first_window_page(y, T);
+        if (n == 0) continue;
+        pl.seqs[pl.nseq] = seq_ids[i];
+        pl.lens[pl.nseq++] = T;
+        if (n <= small_tokens) {
+            SmallParams &p = pl.s;
+            const int j = p.nseq++;
+            p.seqs[j] = seq_ids[i]; p.T[j] = T; p.n[j] = n; p.off[j] = off; p.fw[j] = fw;
+        } else if (tensor) {
+            const int j = f.nseq++;
+            f.T[j] = g.T[j] = T;
+            f.n[j] = g.n[j] = n;
+            f.off[j] = g.off[j] = off;
+            g.seqs[j] = seq_ids[i];
+            g.fw[j] = fw;
+            f.blk_off[j + 1] = g.blk_off[j + 1] = f.blk_off[j] + (T + n + FLASH_KEYS - 1) / FLASH_KEYS;
+        } else {
+            const int j = a.nseq++;
+            a.T[j] = T; a.n[j] = n; a.off[j] = off;
+            a.koff[j] = rows;
+            RowsParams &r = pl.r;
+            r.seqs[j] = seq_ids[i]; r.T[j] = T; r.n[j] = T + n; r.off[j] = (int)rows; r.coff[j] = off;
+            rows += T + n;
             tiles += (long)y.H * ((n * (long)y.G + 31) / 32);
-            ++a.nseq;
         }
-        off += n;
     }
-    if (a.nseq == 0) return;
-    if (y.dtype == 1 && !y.q4) {
-        pl.flash = true;
-        plan_flash(s, pl);
-        return;
+    g.nseq = f.nseq;
+    pl.r.nseq = a.nseq;
+    size_t at = 0;
+    if (pl.s.nseq) {
+        SmallParams &p = pl.s;
+        split_small(s, p);
+        a.nseq = p.nseq;  // merged by the same kernel
+        for (int j = 0; j < p.nseq; ++j) {
+            a.T[j] = p.T[j]; a.n[j] = p.n[j]; a.off[j] = p.off[j];
+            a.ns[j] = p.ns[j];
+            a.poff[j] = p.poff[j] = parts;
+            if (p.ns[j] > 1) parts += (long long)y.H * p.ns[j] * p.n[j] * y.G;
+        }
     }
-    // few query tiles: cut the keys so that about four CTAs land on every SM
-    const int want = tiles > 0 ? (int)std::max(1L, 4L * s->num_sms / tiles) : 1;
-    long long parts = 0;
-    for (int j = 0; j < a.nseq; ++j) {
-        a.ns[j] = std::max(1, std::min(want, (a.T[j] + a.n[j]) / 64));
-        a.poff[j] = parts;
-        if (a.ns[j] > 1) parts += (long long)y.H * a.ns[j] * a.n[j] * y.G;
+    if (f.nseq) {
+        split_flash(s, f);
+        const size_t blocks = (size_t)f.blk_off[f.nseq] * y.H;
+        pl.images = at;
+        pl.scales = pl.images + blocks * (2 * FLASH_KEYS * y.d * 2);
+        pl.flash_parts = pl.scales + up256(blocks * sizeof(float2));
+        at = pl.flash_parts + (f.ctas > 1 ? up256((size_t)2 * f.ctas * FLASH_ROWS * (y.d + 4) * 4) : 0);
     }
-    const size_t rows_bytes = (size_t)pl.rows * y.H * y.d * y.esz;
-    pl.v_off = up256(rows_bytes);
-    pl.part_off = pl.v_off + up256(rows_bytes);
-    pl.bytes = pl.part_off + up256((size_t)parts * (y.d + 4) * 4);
+    if (rows) {
+        // few query tiles: cut the keys so that about four CTAs land on every SM
+        const int want = (int)std::max(1L, 4L * s->num_sms / tiles);
+        for (int j = 0; j < a.nseq; ++j) {
+            a.ns[j] = std::max(1, std::min(want, (a.T[j] + a.n[j]) / 64));
+            a.poff[j] = parts;
+            if (a.ns[j] > 1) parts += (long long)y.H * a.ns[j] * a.n[j] * y.G;
+        }
+        const size_t bytes = up256((size_t)rows * y.H * y.d * y.esz);
+        pl.keys = at;
+        pl.values = at + bytes;
+        at += 2 * bytes;
+    }
+    pl.parts = at;
+    pl.bytes = at + up256((size_t)parts * (y.d + 4) * 4);
 }
 
 // Pages of an appended sequence that leave the dense region without factors.
@@ -204,17 +296,6 @@ size_t gather_bytes(const Layout &y, const LeavePlan &lp) {
     return 2 * up256(rows * y.H * y.d * y.esz);
 }
 
-void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
-    rp = RowsParams{};
-    rp.y = s->y;
-    rp.factor_pool = s->factor_pool;
-    rp.dense_pool = s->dense_pool;
-    rp.rope_base = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_base_offset);
-    rp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_delta_offset);
-    rp.layer = layer;
-    rp.turn = 1;
-}
-
 puzzlekv_status check_work(const void *work, size_t have, size_t need) {
     if (need == 0) return PUZZLEKV_OK;
     if (!work || (reinterpret_cast<uintptr_t>(work) & 255u) != 0)
@@ -236,7 +317,7 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *s, int32_t layer,
         if (attention_bytes) {
             AttnPlan pl;
             plan_attention(s, layer, seq_ids, counts, B, pl);
-            *attention_bytes = pl.a.nseq ? pl.bytes : 0;
+            *attention_bytes = pl.bytes;
         }
         if (append_bytes) {
             *append_bytes = 0;
@@ -262,74 +343,58 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
         const Layout &y = s->y;
         AttnPlan pl;
         plan_attention(s, layer, seq_ids, counts, B, pl);
-        ChunkAttnParams &a = pl.a;
-        if (a.nseq == 0) return PUZZLEKV_OK;
+        if (pl.nseq == 0) return PUZZLEKV_OK;
         st = check_work(work, work_bytes, pl.bytes);
         if (st != PUZZLEKV_OK) return st;
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
         char *w = static_cast<char *>(work);
-        wait_conversions(s, strm, pl.seq, a.T, a.nseq);
-        if (pl.flash) {
-            StageParams sp{};
-            sp.y = y;
-            sp.factor_pool = s->factor_pool;
-            sp.dense_pool = s->dense_pool;
-            sp.rope_base = reinterpret_cast<const float2 *>(s->workspace + y.rope_base_offset);
-            sp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + y.rope_delta_offset);
-            sp.k_new = static_cast<const char *>(k);
-            sp.v_new = static_cast<const char *>(v);
-            sp.images = w;
-            sp.scales = reinterpret_cast<float2 *>(w + pl.scale_off);
-            sp.status = status_ptr(s);
-            sp.layer = layer;
-            sp.nseq = a.nseq;
-            for (int j = 0; j < a.nseq; ++j) {
-                sp.seqs[j] = pl.seq[j];
-                sp.T[j] = a.T[j];
-                sp.n[j] = a.n[j];
-                sp.off[j] = a.off[j];
-                sp.fw[j] = first_window_page(y, a.T[j]);
-                sp.blk_off[j + 1] = pl.f.blk_off[j + 1];
-            }
-            FlashParams &f = pl.f;
-            f.q = static_cast<const char *>(q);
-            f.out = static_cast<char *>(out);
-            f.images = w;
-            f.scales = sp.scales;
-            f.partials = reinterpret_cast<float *>(w + pl.part_off);
-            f.status = status_ptr(s);
-            s->after_decode = false;
-            cudaError_t e = launch_stage(sp, s->num_sms, strm);
-            if (e == cudaSuccess) e = launch_flash(f, y.d, strm);
-            if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-            return PUZZLEKV_OK;
+        wait_conversions(s, strm, pl.seqs, pl.lens, pl.nseq);
+        s->after_decode = false;
+        cudaError_t e = cudaSuccess;
+        if (pl.f.nseq) {
+            pl.g.k_new = static_cast<const char *>(k);
+            pl.g.v_new = static_cast<const char *>(v);
+            pl.g.images = w + pl.images;
+            pl.g.scales = reinterpret_cast<float2 *>(w + pl.scales);
+            pl.g.status = status_ptr(s);
+            pl.f.q = static_cast<const char *>(q);
+            pl.f.out = static_cast<char *>(out);
+            pl.f.images = pl.g.images;
+            pl.f.scales = pl.g.scales;
+            pl.f.partials = reinterpret_cast<float *>(w + pl.flash_parts);
+            pl.f.status = status_ptr(s);
+            e = launch_stage(pl.g, s->num_sms, strm);
+            if (e == cudaSuccess) e = launch_flash(pl.f, y.d, strm);
         }
-        RowsParams rp;
-        rows_params(s, layer, rp);
-        rp.k_new = static_cast<const char *>(k);
-        rp.v_new = static_cast<const char *>(v);
-        rp.k_out = w;
-        rp.v_out = w + pl.v_off;
-        rp.row_stride = (size_t)y.H * y.d;
-        rp.head_stride = y.d;
-        rp.nseq = a.nseq;
-        for (int j = 0; j < a.nseq; ++j) {
-            rp.seqs[j] = pl.seq[j];
-            rp.T[j] = a.T[j];
-            rp.lo[j] = 0;
-            rp.n[j] = a.T[j] + a.n[j];
-            rp.off[j] = (int)a.koff[j];
-            rp.coff[j] = a.off[j];
-        }
+        ChunkAttnParams &a = pl.a;
         a.q = static_cast<const char *>(q);
         a.out = static_cast<char *>(out);
-        a.K = w;
-        a.V = w + pl.v_off;
-        a.partials = reinterpret_cast<float *>(w + pl.part_off);
-        s->after_decode = false;
-        cudaError_t e = launch_rows(rp, strm);
-        if (e == cudaSuccess) e = launch_chunk_simple(a, y.dtype, strm);
-        if (e == cudaSuccess) e = launch_chunk_merge(a, y.dtype, strm);
+        a.partials = reinterpret_cast<float *>(w + pl.parts);
+        if (pl.s.nseq && e == cudaSuccess) {
+            pl.s.factor_pool = s->factor_pool;
+            pl.s.dense_pool = s->dense_pool;
+            pl.s.q = a.q;
+            pl.s.k_new = static_cast<const char *>(k);
+            pl.s.v_new = static_cast<const char *>(v);
+            pl.s.out = a.out;
+            pl.s.partials = a.partials;
+            pl.s.status = status_ptr(s);
+            e = launch_small(pl.s, strm);
+        }
+        if (pl.r.nseq && e == cudaSuccess) {
+            RowsParams &r = pl.r;
+            r.k_new = static_cast<const char *>(k);
+            r.v_new = static_cast<const char *>(v);
+            r.k_out = w + pl.keys;
+            r.v_out = w + pl.values;
+            r.row_stride = (size_t)y.H * y.d;
+            r.head_stride = y.d;
+            a.K = r.k_out;
+            a.V = r.v_out;
+            e = launch_rows(r, strm);
+            if (e == cudaSuccess) e = launch_chunk_simple(a, y.dtype, strm);
+        }
+        if (a.nseq && e == cudaSuccess) e = launch_chunk_merge(a, y.dtype, strm);
         if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
         return PUZZLEKV_OK;
     });

@@ -1,0 +1,501 @@
+// Chunk attention of a few tokens per sequence ("PuzzleKV: Page-Wise Low-Rank
+// Decomposition for KV Cache Compression", §3.3 ④, eqs. (4)-(5)): drafted
+// tokens being verified, or single tokens beside longer chunks.
+//
+// HBM-bound: the pages are read once, as stored, for all query rows of the KV
+// head.  A factorized page contributes s = (q R_K^T) L_K^T and o = (p L_V) R_V,
+// the small factors contracted first (no page is rebuilt).  Rebuilding pages
+// for the tensor-memory kernel (chunk_flash.cu) costs three times their bytes
+// and pays only when hundreds of rows share a page.
+//
+// The products run as m16n8k16 on 16-row tiles of the queries: they are too
+// narrow (ranks of 16 to 24, 16 to 128 rows) to fill a 128-row tensor-memory
+// tile, and the intermediates feed the next product from registers.  The
+// intermediates (q R_K^T, the weights, and their product with L_V) are split
+// into bf16 high parts and residuals, two products on one operand, so that no
+// step rounds to fewer than 16 bits; the output is rounded once.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace pkv {
+
+namespace {
+
+constexpr int SMALL_WARPS = 8;
+constexpr int SMALL_SLOTS = 16;
+
+struct SmallShared {
+    uint64_t full[SMALL_SLOTS], empty[SMALL_SLOTS];
+    int failed;
+};
+
+__device__ __forceinline__ float ex2s(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// One warp's running state for its 16 query rows: lane 4g + c holds rows g and
+// g + 8, columns 8 t + 2c, + 1 of every tile t.
+template <int D>
+struct RowState {
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+};
+
+// Fold the scores of NT token tiles into the state; they become weights.
+template <int NT, int D>
+__device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4]) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mx = fmaxf(mx, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(w.m[r], mx), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2s(w.m[r] - base);
+        float ls = 0.f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[t][2 * r + e] = ex2s(s[t][2 * r + e] - base);
+                ls += s[t][2 * r + e];
+            }
+        w.l[r] = fmaf(w.l[r], f, ls);  // this lane's columns; the quad's sums join at the end
+        w.m[r] = mn;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+            w.o[t][2 * r] *= f;
+            w.o[t][2 * r + 1] *= f;
+        }
+    }
+}
+
+// A operand (high parts and residuals) of two adjacent accumulator tiles.
+__device__ __forceinline__ void split_tiles(const float *t0, const float *t1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    split_bf16(t0[0], t0[1], hi[0], lo[0]);
+    split_bf16(t0[2], t0[3], hi[1], lo[1]);
+    split_bf16(t1[0], t1[1], hi[2], lo[2]);
+    split_bf16(t1[2], t1[3], hi[3], lo[3]);
+}
+
+// A factorized page, eq. (4).
+template <int P, int D>
+__device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint32_t rec, float scale, int lane) {
+    constexpr int NT = P / 8;
+    const int row8 = (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+    {
+        const uint32_t LK = rec, RK = rec + (uint32_t)y.off_RK;
+        const int pitch = y.rkp * 2;
+        int k0 = 0;
+#pragma unroll 1
+        for (; k0 + 16 <= y.rkp; k0 += 16) {
+            float t[4][4] = {};  // even and odd steps apart: shorter chains
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(RK + swz_offset(k0 + row8, 32 * ks + 16 * half, D * 2), b0, b1, b2, b3);
+                mma16816(t[2 * (ks & 1)], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
+                mma16816(t[2 * (ks & 1) + 1], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b2, b3);
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                t[0][e] += t[2][e];
+                t[1][e] += t[3][e];
+            }
+            split_tiles(t[0], t[1], hi, lo);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(LK + swz_offset(8 * n + row8, 2 * k0 + 16 * half, pitch), b0, b1, b2, b3);
+                mma16816(s[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
+                mma16816(s[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
+                mma16816(s[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
+                mma16816(s[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
+            }
+        }
+        if (k0 < y.rkp) {  // eight ranks left
+            float t[2][4] = {};
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks += 2) {
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(RK + swz_offset(k0 + (lane & 7), 32 * ks + 16 * (lane >> 3), D * 2), b0, b1, b2, b3);
+                mma16816(t[0], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
+                mma16816(t[1], w.q[ks + 1][0], w.q[ks + 1][1], w.q[ks + 1][2], w.q[ks + 1][3], b2, b3);
+            }
+            uint32_t h0, h1, l0, l1;
+            split_bf16(t[0][0] + t[1][0], t[0][1] + t[1][1], h0, l0);
+            split_bf16(t[0][2] + t[1][2], t[0][3] + t[1][3], h1, l1);
+#pragma unroll
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t b0, b1;
+                ldsm_x2(LK + swz_offset(8 * n + (lane & 15), 2 * k0, pitch), b0, b1);
+                mma1688(s[n], h0, h1, b0);
+                mma1688(s[n + 1], h0, h1, b1);
+                mma1688(s[n], l0, l1, b0);
+                mma1688(s[n + 1], l0, l1, b1);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] *= scale;
+    fold<NT, D>(w, s);
+    uint32_t ph[P / 16][4], pl[P / 16][4];
+#pragma unroll
+    for (int k = 0; k < P / 16; ++k) split_tiles(s[2 * k], s[2 * k + 1], ph[k], pl[k]);
+    const uint32_t LV = rec + (uint32_t)y.off_LV, RV = rec + (uint32_t)y.off_RV;
+    const int pitch = y.rvp * 2;
+    int k0 = 0;
+#pragma unroll 1
+    for (; k0 + 16 <= y.rvp; k0 += 16) {
+        float u[4][4] = {};  // weights' high parts and residuals apart
+#pragma unroll
+        for (int k = 0; k < P / 16; ++k) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(LV + swz_offset(k0 + row8, 32 * k + 16 * half, P * 2), b0, b1, b2, b3);
+            mma16816(u[0], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b0, b1);
+            mma16816(u[1], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b2, b3);
+            mma16816(u[2], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b0, b1);
+            mma16816(u[3], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b2, b3);
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            u[0][e] += u[2][e];
+            u[1][e] += u[3][e];
+        }
+        split_tiles(u[0], u[1], hi, lo);
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(RV + swz_offset(8 * n + row8, 2 * k0 + 16 * half, pitch), b0, b1, b2, b3);
+            mma16816(w.o[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
+            mma16816(w.o[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
+            mma16816(w.o[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
+            mma16816(w.o[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
+        }
+    }
+    if (k0 < y.rvp) {
+        float u[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < P / 16; ++k) {
+            uint32_t b0, b1;
+            ldsm_x2(LV + swz_offset(k0 + (lane & 7), 32 * k + 16 * half, P * 2), b0, b1);
+            mma16816(u[0], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b0, b1);
+            mma16816(u[1], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b0, b1);
+        }
+        uint32_t h0, h1, l0, l1;
+        split_bf16(u[0][0] + u[1][0], u[0][1] + u[1][1], h0, l0);
+        split_bf16(u[0][2] + u[1][2], u[0][3] + u[1][3], h1, l1);
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 4) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(RV + swz_offset(8 * n + lane, 2 * k0, pitch), b0, b1, b2, b3);
+            mma1688(w.o[n], h0, h1, b0);
+            mma1688(w.o[n + 1], h0, h1, b1);
+            mma1688(w.o[n + 2], h0, h1, b2);
+            mma1688(w.o[n + 3], h0, h1, b3);
+            mma1688(w.o[n], l0, l1, b0);
+            mma1688(w.o[n + 1], l0, l1, b1);
+            mma1688(w.o[n + 2], l0, l1, b2);
+            mma1688(w.o[n + 3], l0, l1, b3);
+        }
+    }
+}
+
+// UR dense rows at `rows` (keys, then values UR rows further), of which row g
+// (g + 8) of the tile sees the first see[0] (see[1]) and `valid` hold anything.
+template <int UR, int D>
+__device__ __forceinline__ void dense_unit(RowState<D> &w, uint32_t rows, int see0, int see1, int valid, float scale, int lane) {
+    constexpr int NT = UR / 8;
+    const int c = lane & 3, row8 = (lane & 7) + 8 * (lane >> 4), half = (lane >> 3) & 1;
+    float s[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4(rows + swz_offset(8 * n + row8, 32 * ks + 16 * half, D * 2), b0, b1, b2, b3);
+            mma16816(s[n], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
+            mma16816(s[n + 1], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b2, b3);
+        }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int col = 8 * t + 2 * c + (e & 1);
+            s[t][e] = col < (e < 2 ? see0 : see1) ? s[t][e] * scale : -INFINITY;
+        }
+    fold<NT, D>(w, s);
+    const uint32_t V = rows + UR * D * 2;
+#pragma unroll
+    for (int k = 0; k < UR / 16; ++k) {
+        uint32_t hi[4], lo[4];
+        split_tiles(s[2 * k], s[2 * k + 1], hi, lo);
+        // rows past `valid` hold old values, whatever they are: read as zero
+        auto keep = [&](int t) { return (t < valid ? 0xffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u); };
+        const uint32_t k0 = keep(16 * k + 2 * c), k1 = keep(16 * k + 8 + 2 * c);
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(V + swz_offset(16 * k + (lane & 15), 16 * n + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
+            b0 &= k0;
+            b1 &= k1;
+            b2 &= k0;
+            b3 &= k1;
+            mma16816(w.o[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
+            mma16816(w.o[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
+            mma16816(w.o[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
+            mma16816(w.o[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
+        }
+    }
+}
+
+}  // namespace
+
+// Eight warps: RT row tiles (16 rows each) x PG page groups.  A group's warps
+// work on the same unit, a factorized page or UR rows of a dense page, each for
+// its rows; the groups take the CTA's units in turn and stream them through
+// slots of their own, filled by bulk copies that the group's first warp issues
+// as soon as all its warps have left the slot.
+template <int P, int D>
+__global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallParams p) {
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ SmallShared sh;
+    constexpr int UR = P / 2 < 16 ? 16 : P / 2, UP = P / UR;  // rows of a dense unit, units of a page
+    constexpr uint32_t HALF = UR * D * 2;                    // its key (or value) bytes
+    const Layout &y = p.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int h = blockIdx.y;
+    int i = 0;
+    while ((int)blockIdx.x >= p.boff[i + 1] - (i + 1)) ++i;
+    const int sp = (int)blockIdx.x - (p.boff[i] - i), ns = p.ns[i];
+    const int G = y.G, n = p.n[i], R = n * G, T = p.T[i], b = p.seqs[i];
+    const int tiles = (R + 15) / 16, RT = tiles <= 1 ? 1 : tiles <= 2 ? 2 : tiles <= 4 ? 4 : 8;
+    const int PG = min(SMALL_WARPS / RT, p.slots / 2), SPG = p.slots / PG;
+    const int rt = warp % RT, pg = warp / RT;
+    // the CTA's units: dense sink pages, factorized pages, dense window pages
+    const int p0 = p.bounds[p.boff[i] + sp], p1 = p.bounds[p.boff[i] + sp + 1];
+    const int n_pages = (T + P - 1) / P, fw = max(p.fw[i], 0), fs = min(y.sink_pages, n_pages);
+    auto dense_units = [&](int a, int z) {  // units of the dense pages [a, z)
+        return a < z ? UP * (z - a) - (z == n_pages ? UP - (T - (n_pages - 1) * P + UR - 1) / UR : 0) : 0;
+    };
+    const int a1 = min(p1, fs), f0 = max(p0, fs), f1 = max(f0, min(p1, fw)), w0 = max(f1, max(p0, fs));
+    const int uA = dense_units(p0, a1), uF = f1 - f0, uW = w0 < p1 ? dense_units(w0, p1) : 0;
+    const int units = uA + uF + uW;
+    // unit u: page and, for dense pages, first row in the page (factorized: -1)
+    auto unit = [&](int u, int &page, int &row) {
+        if (u < uA) {
+            page = p0 + u / UP;
+            row = u % UP * UR;
+        } else if (u < uA + uF) {
+            page = f0 + u - uA;
+            row = -1;
+        } else {
+            const int k = u - uA - uF;
+            page = w0 + k / UP;
+            row = k % UP * UR;
+        }
+    };
+    if (tid == 0) {
+        for (int k = 0; k < p.slots; ++k) {
+            mbar_init(&sh.full[k], 1);
+            mbar_init(&sh.empty[k], RT);
+        }
+        sh.failed = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const int slot0 = pg * SPG;
+    const bool active = pg < PG, leader = active && rt == 0 && lane == 0;
+    auto slot_of = [&](int k) { return slot0 + k % SPG; };
+    // Leader: the group's k-th unit into its slot.
+    auto issue = [&](int k) {
+        const int u = pg + k * PG;
+        if (u >= units) return true;
+        const int sl = slot_of(k);
+        if (k >= SPG && !mbar_wait_bounded(&sh.empty[sl], (k / SPG - 1) & 1, p.status)) return false;
+        int page, row;
+        unit(u, page, row);
+        unsigned char *dst = sm + (size_t)sl * p.unit_bytes;
+        if (row < 0) {
+            mbar_arrive_expect_tx(&sh.full[sl], (uint32_t)y.rec_bytes);
+            bulk_g2s(dst, p.factor_pool + y.record_offset(p.layer, b, h, page), (uint32_t)y.rec_bytes, &sh.full[sl]);
+        } else {
+            const char *src = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(page), h, 0) + (size_t)row * D * 2;
+            mbar_arrive_expect_tx(&sh.full[sl], 2 * HALF);
+            bulk_g2s(dst, src, HALF, &sh.full[sl]);
+            bulk_g2s(dst + HALF, src + y.dense_half_bytes, HALF, &sh.full[sl]);
+        }
+        return true;
+    };
+    bool ok = true;
+    int issued = 0;
+    if (leader)
+        for (; issued < SPG; ++issued) issue(issued);
+    // the chunk's rows, swizzled, zeros past the last: units of UR rows
+    unsigned char *chunk = sm + (size_t)p.slots * p.unit_bytes;
+    const int cu = sp == ns - 1 ? (n + UR - 1) / UR : 0;
+    for (int e = tid; e < cu * UR * 2 * (D / 8); e += blockDim.x) {
+        const int ch = e % (D / 8), kv = e / (D / 8) % 2, t = e / (D / 4), u = t / UR, r = t % UR;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (t < n) v = reinterpret_cast<const uint4 *>((kv ? p.v_new : p.k_new) + ((size_t)(p.off[i] + t) * y.H + h) * (D * 2))[ch];
+        *reinterpret_cast<uint4 *>(chunk + (size_t)u * 2 * HALF + kv * HALF + swz_offset(r, 16 * ch, D * 2)) = v;
+    }
+    // the warp's query rows
+    RowState<D> w;
+    const int r0 = 16 * rt + g;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int r = r0 + 8 * (e & 1), col = 16 * k + 2 * c + 8 * (e >> 1);
+            w.q[k][e] = r < R ? *reinterpret_cast<const uint32_t *>(
+                                    p.q + ((((size_t)(p.off[i] + r / G) * y.Hq + h * G + r % G) * D) + col) * 2)
+                              : 0u;
+        }
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) w.o[t][0] = w.o[t][1] = w.o[t][2] = w.o[t][3] = 0.f;
+    w.m[0] = w.m[1] = -INFINITY;
+    w.l[0] = w.l[1] = 0.f;
+    if (cu) __syncthreads();  // the chunk is in place (the same in every thread)
+    if (active) {
+        for (int u = pg; u < cu; u += PG)
+            dense_unit<UR, D>(w, smem_u32(chunk + (size_t)u * 2 * HALF), r0 / G + 1 - u * UR, (r0 + 8) / G + 1 - u * UR, UR,
+                              p.scale_log2, lane);
+        for (int k = 0; pg + k * PG < units; ++k) {
+            const int sl = slot_of(k);
+            // a warp leaves as one
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[sl], (k / SPG) & 1, p.status)) != 0;
+            if (!ok) break;
+            int page, row;
+            unit(pg + k * PG, page, row);
+            const uint32_t at = smem_u32(sm + (size_t)sl * p.unit_bytes);
+            if (row < 0) {
+                page_unit<P, D>(w, y, at, p.scale_log2, lane);
+            } else {
+                const int valid = min(UR, T - page * P - row);
+                dense_unit<UR, D>(w, at, valid, valid, valid, p.scale_log2, lane);
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[sl]);
+            if (leader) {
+                ok = issue(issued);
+                if (ok) ++issued;
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+        }
+        if (!ok) {
+            if (leader)  // copies still in flight land before the CTA ends
+                for (int k = max(0, issued - SPG); k < issued; ++k)
+                    if (pg + k * PG < units) mbar_wait_bounded(&sh.full[slot_of(k)], (k / SPG) & 1, nullptr);
+            if (lane == 0) atomicExch(&sh.failed, 1);
+        }
+    }
+    __syncthreads();  // every copy has landed and every slot is read
+    if (sh.failed) return;
+    // the groups' states side by side, then joined row by row, eq. (5)
+    constexpr int S = D + 4;
+    float *comb = reinterpret_cast<float *>(sm);
+    if (active) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 1);
+            w.l[r] += __shfl_xor_sync(0xffffffffu, w.l[r], 2);
+            float *row = comb + ((size_t)pg * RT * 16 + r0 + 8 * r) * S;
+            if (c == 0) *reinterpret_cast<float2 *>(row) = make_float2(w.m[r], w.l[r]);
+#pragma unroll
+            for (int t = 0; t < D / 8; ++t)
+                *reinterpret_cast<float2 *>(row + 4 + 8 * t + 2 * c) = make_float2(w.o[t][2 * r], w.o[t][2 * r + 1]);
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < R * (D / 4); e += blockDim.x) {
+        const int r = e / (D / 4), j = e % (D / 4);
+        float M = -INFINITY;
+        for (int k = 0; k < PG; ++k) M = fmaxf(M, comb[((size_t)k * RT * 16 + r) * S]);
+        float L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < PG; ++k) {
+            const float *row = comb + ((size_t)k * RT * 16 + r) * S;
+            const float f = row[0] == -INFINITY ? 0.f : ex2s(row[0] - M);
+            const float4 v = *reinterpret_cast<const float4 *>(row + 4 + 4 * j);
+            L = fmaf(f, row[1], L);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        if (ns == 1) {
+            const float il = 1.f / L;
+            *reinterpret_cast<uint2 *>(p.out + ((((size_t)(p.off[i] + r / G) * y.Hq + h * G + r % G) * D) + 4 * j) * 2) =
+                make_uint2(pack_bf16(o.x * il, o.y * il), pack_bf16(o.z * il, o.w * il));
+        } else {
+            float *row = p.partials + (size_t)(p.poff[i] + (long long)(h * ns + sp) * R + r) * S;
+            if (j == 0) *reinterpret_cast<float4 *>(row) = make_float4(M, L, 0.f, 0.f);
+            *reinterpret_cast<float4 *>(row + 4 + 4 * j) = o;
+        }
+    }
+}
+
+static int small_unit_bytes(const Layout &y) {
+    const int ur = y.P / 2 < 16 ? 16 : y.P / 2;
+    return (int)((std::max(y.rec_bytes, (size_t)ur * y.d * 4) + 127) & ~(size_t)127);
+}
+// Shared memory: slots, the chunk's rows; the states of eight row tiles reuse it.
+static int small_slots(const Layout &y, int most_tokens, int &chunk_bytes) {
+    const int ur = y.P / 2 < 16 ? 16 : y.P / 2;
+    chunk_bytes = (most_tokens + ur - 1) / ur * ur * y.d * 4;
+    const int room = 226 * 1024 - (int)sizeof(SmallShared) - chunk_bytes;
+    return std::min(SMALL_SLOTS, room / small_unit_bytes(y));
+}
+
+size_t small_smem_bytes(const Layout &y, int most_tokens) {
+    int chunk = 0;
+    const int slots = small_slots(y, most_tokens, chunk);
+    if (slots < 2) return 0;
+    return std::max((size_t)slots * small_unit_bytes(y) + chunk, (size_t)SMALL_ROWS * (y.d + 4) * 4);
+}
+
+template <int P, int D>
+static cudaError_t small_t(const SmallParams &p, size_t smem, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(small_kernel<P, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    small_kernel<P, D><<<dim3((unsigned)(p.boff[p.nseq] - p.nseq), (unsigned)p.y.H), 32 * SMALL_WARPS, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_small(SmallParams &p, cudaStream_t st) {
+    if (p.nseq == 0) return cudaSuccess;
+    int most = 0;
+    for (int i = 0; i < p.nseq; ++i) most = std::max(most, p.n[i]);
+    const size_t smem = small_smem_bytes(p.y, most);
+    if (smem == 0) return cudaErrorInvalidValue;
+    p.slots = small_slots(p.y, most, p.chunk_bytes);
+    p.unit_bytes = small_unit_bytes(p.y);
+    if (p.y.d == 64) {
+        if (p.y.P == 16) return small_t<16, 64>(p, smem, st);
+        if (p.y.P == 32) return small_t<32, 64>(p, smem, st);
+        return small_t<64, 64>(p, smem, st);
+    }
+    if (p.y.P == 16) return small_t<16, 128>(p, smem, st);
+    if (p.y.P == 32) return small_t<32, 128>(p, smem, st);
+    return small_t<64, 128>(p, smem, st);
+}
+
+}  // namespace pkv

@@ -240,6 +240,33 @@ PKV_HD int flash_blocks(int T, int n, int G, int p) {
     return (T + (last - 1) / G) / FLASH_KEYS + 1;
 }
 
+// Attention of a few tokens per sequence straight over the pages (bf16 stores
+// with keys as stored): CTA (split, KV head) streams the units of its entry's
+// pages [bounds[boff + split], bounds[boff + split + 1]) for all the entry's
+// query rows; the last split also takes the chunk.  States of entries with
+// several splits go to the rows of ChunkAttnParams::partials.
+constexpr int SMALL_ROWS = 128;        // query rows per (entry, KV head)
+constexpr int SMALL_BOUNDS = 1024;
+struct SmallParams {
+    Layout y;
+    const char *factor_pool, *dense_pool;
+    const char *q, *k_new, *v_new;
+    char *out;
+    float *partials;
+    int *status;
+    float scale_log2;
+    int layer, nseq;
+    int slots, unit_bytes, chunk_bytes;  // filled by the launcher
+    int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH], ns[MAX_CALL_BATCH];
+    int fw[MAX_CALL_BATCH];
+    int boff[MAX_CALL_BATCH + 1];  // first bound of each entry; split numbers run boff[i] - i ..
+    long long poff[MAX_CALL_BATCH];
+    int bounds[SMALL_BOUNDS];
+};
+// Shared memory that a launch for these entries would take (0: they do not fit).
+size_t small_smem_bytes(const Layout &y, int most_tokens);
+cudaError_t launch_small(SmallParams &p, cudaStream_t st);
+
 cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st);
 
