@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
 // split order (the same sums whatever the launch), eq. (5).
 template <typename T, int D>
 __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkAttnParams p) {
+    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     int i = 0;
@@ -212,14 +213,11 @@ cudaError_t launch_chunk_merge(const ChunkAttnParams &q, int dtype, cudaStream_t
     const int rows = p.tile_off[p.nseq];
     if (rows == 0) return cudaSuccess;
     const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (dtype == 1) {
-        if (p.d == 64) chunk_merge_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
-        else chunk_merge_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p);
-    } else {
-        if (p.d == 64) chunk_merge_kernel<float, 64><<<grid, 128, 0, st>>>(p);
-        else chunk_merge_kernel<float, 128><<<grid, 128, 0, st>>>(p);
-    }
-    return cudaGetLastError();
+    if (dtype == 1)
+        return p.d == 64 ? launch_dependent(chunk_merge_kernel<__nv_bfloat16, 64>, grid, 128, 0, st, p)
+                         : launch_dependent(chunk_merge_kernel<__nv_bfloat16, 128>, grid, 128, 0, st, p);
+    return p.d == 64 ? launch_dependent(chunk_merge_kernel<float, 64>, grid, 128, 0, st, p)
+                     : launch_dependent(chunk_merge_kernel<float, 128>, grid, 128, 0, st, p);
 }
 
 }  // namespace pkv

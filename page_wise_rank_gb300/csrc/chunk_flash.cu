@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
             bulk_g2s(sm + IMG + (buf * NP + s) * page_bytes, src, part, &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
+    grid_launch_dependents();  // the attention may be set up
     uint32_t phase = 0;  // bit of each buffer's barrier
     int buf = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
@@ -461,6 +462,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    grid_dependency_wait();  // the images are written
     const uint32_t tmem = s.tmem;
     Pieces pc(p, blockIdx.x);
 
@@ -744,6 +746,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
 // every launch.
 template <int D>
 __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
+    grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const FlashParams::Share &cut = p.share[blockIdx.x + 1], &before = p.share[blockIdx.x];
     // units from the pair's first on: cut.b0 before the boundary
@@ -826,13 +829,11 @@ static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
     constexpr int smem = (2 + RING) * FLASH_KEYS * D * 2 + 1024;
     cudaError_t e = cudaFuncSetAttribute(flash_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    flash_kernel<D><<<(unsigned)p.ctas, FLASH_THREADS, smem, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(flash_kernel<D>, dim3((unsigned)p.ctas), FLASH_THREADS, smem, st, p);
     if (e != cudaSuccess || p.ctas == 1) return e;
     int most = 0;
     for (int i = 0; i < p.nseq; ++i) most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
-    flash_merge_kernel<D><<<dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(flash_merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st, p);
 }
 
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st) {

@@ -46,9 +46,10 @@ struct RowState {
     float m[2], l[2];
 };
 
-// Fold the scores of NT token tiles into the state; they become weights.
+// Fold the scores of NT token tiles (in units of 1 / scale log2) into the
+// state; they become weights.
 template <int NT, int D>
-__device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4]) {
+__device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4], float scale) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         float mx = -INFINITY;
@@ -56,25 +57,39 @@ __device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4]) {
         for (int t = 0; t < NT; ++t) mx = fmaxf(mx, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(w.m[r], mx), base = mn == -INFINITY ? 0.f : mn;
+        const float mn = fmaxf(w.m[r], mx * scale), base = mn == -INFINITY ? 0.f : mn;
         const float f = ex2s(w.m[r] - base);
         float ls = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                s[t][2 * r + e] = ex2s(s[t][2 * r + e] - base);
+                s[t][2 * r + e] = ex2s(fmaf(s[t][2 * r + e], scale, -base));
                 ls += s[t][2 * r + e];
             }
         w.l[r] = fmaf(w.l[r], f, ls);  // this lane's columns; the quad's sums join at the end
         w.m[r] = mn;
+        if (__any_sync(0xffffffffu, f != 1.f))
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-            w.o[t][2 * r] *= f;
-            w.o[t][2 * r + 1] *= f;
-        }
+            for (int t = 0; t < D / 8; ++t) {
+                w.o[t][2 * r] *= f;
+                w.o[t][2 * r + 1] *= f;
+            }
     }
 }
+
+// Reads of a swizzled matrix whose rows are `pitch` bytes (set at run time):
+// rows a + 8 n of a lane share their chunk permutation, since eight rows are a
+// whole number of its periods, so it is found once.
+struct Rows {
+    uint32_t at;     // the lane's row a
+    int pitch8, x;   // bytes of eight rows; the permutation
+    __device__ __forceinline__ Rows(uint32_t base, int row, int pitch) : at(base + row * pitch), pitch8(8 * pitch) {
+        const int g = gcd8(pitch >> 4);  // a power of two; the period is 8 / g rows
+        x = (((row & 7) * g) >> 3) & (g - 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(int n, int chunk) const { return at + n * pitch8 + ((chunk ^ x) << 4); }
+};
 
 // A operand (high parts and residuals) of two adjacent accumulator tiles.
 __device__ __forceinline__ void split_tiles(const float *t0, const float *t1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
@@ -82,6 +97,19 @@ __device__ __forceinline__ void split_tiles(const float *t0, const float *t1, ui
     split_bf16(t0[2], t0[3], hi[1], lo[1]);
     split_bf16(t1[0], t1[1], hi[2], lo[2]);
     split_bf16(t1[2], t1[3], hi[3], lo[3]);
+}
+
+// NT tiles += (hi + lo) b: the high parts' products, then the residuals', so
+// that products on one tile are NT apart.
+template <int NT>
+__device__ __forceinline__ void both(float (*acc)[4], const uint32_t (&hi)[4], const uint32_t (&lo)[4],
+                                     const uint32_t (&b)[NT / 2][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        mma16816(acc[n], hi[0], hi[1], hi[2], hi[3], b[n / 2][2 * (n & 1)], b[n / 2][2 * (n & 1) + 1]);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        mma16816(acc[n], lo[0], lo[1], lo[2], lo[3], b[n / 2][2 * (n & 1)], b[n / 2][2 * (n & 1) + 1]);
 }
 
 // A factorized page, eq. (4).
@@ -93,8 +121,8 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
 #pragma unroll
     for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
     {
-        const uint32_t LK = rec, RK = rec + (uint32_t)y.off_RK;
-        const int pitch = y.rkp * 2;
+        const uint32_t RK = rec + (uint32_t)y.off_RK;
+        const Rows LK(rec, row8, y.rkp * 2), LK8(rec, lane & 15, y.rkp * 2);
         int k0 = 0;
 #pragma unroll 1
         for (; k0 + 16 <= y.rkp; k0 += 16) {
@@ -113,15 +141,10 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
                 t[1][e] += t[3][e];
             }
             split_tiles(t[0], t[1], hi, lo);
+            uint32_t b[NT / 2][4];
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(LK + swz_offset(8 * n + row8, 2 * k0 + 16 * half, pitch), b0, b1, b2, b3);
-                mma16816(s[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
-                mma16816(s[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
-                mma16816(s[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
-                mma16816(s[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
-            }
+            for (int n = 0; n < NT / 2; ++n) ldsm_x4(LK(2 * n, k0 / 8 + half), b[n][0], b[n][1], b[n][2], b[n][3]);
+            both<NT>(s, hi, lo, b);
         }
         if (k0 < y.rkp) {  // eight ranks left
             float t[2][4] = {};
@@ -138,7 +161,7 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
 #pragma unroll
             for (int n = 0; n < NT; n += 2) {
                 uint32_t b0, b1;
-                ldsm_x2(LK + swz_offset(8 * n + (lane & 15), 2 * k0, pitch), b0, b1);
+                ldsm_x2(LK8(n, k0 / 8), b0, b1);
                 mma1688(s[n], h0, h1, b0);
                 mma1688(s[n + 1], h0, h1, b1);
                 mma1688(s[n], l0, l1, b0);
@@ -146,16 +169,12 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
             }
         }
     }
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] *= scale;
-    fold<NT, D>(w, s);
+    fold<NT, D>(w, s, scale);
     uint32_t ph[P / 16][4], pl[P / 16][4];
 #pragma unroll
     for (int k = 0; k < P / 16; ++k) split_tiles(s[2 * k], s[2 * k + 1], ph[k], pl[k]);
-    const uint32_t LV = rec + (uint32_t)y.off_LV, RV = rec + (uint32_t)y.off_RV;
-    const int pitch = y.rvp * 2;
+    const uint32_t LV = rec + (uint32_t)y.off_LV;
+    const Rows RV(rec + (uint32_t)y.off_RV, row8, y.rvp * 2), RV8(rec + (uint32_t)y.off_RV, lane, y.rvp * 2);
     int k0 = 0;
 #pragma unroll 1
     for (; k0 + 16 <= y.rvp; k0 += 16) {
@@ -177,13 +196,11 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
         }
         split_tiles(u[0], u[1], hi, lo);
 #pragma unroll
-        for (int n = 0; n < D / 8; n += 2) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(RV + swz_offset(8 * n + row8, 2 * k0 + 16 * half, pitch), b0, b1, b2, b3);
-            mma16816(w.o[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
-            mma16816(w.o[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
-            mma16816(w.o[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
-            mma16816(w.o[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
+        for (int n0 = 0; n0 < D / 8; n0 += 8) {
+            uint32_t b[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) ldsm_x4(RV(n0 + 2 * n, k0 / 8 + half), b[n][0], b[n][1], b[n][2], b[n][3]);
+            both<8>(w.o + n0, hi, lo, b);
         }
     }
     if (k0 < y.rvp) {
@@ -201,7 +218,7 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
 #pragma unroll
         for (int n = 0; n < D / 8; n += 4) {
             uint32_t b0, b1, b2, b3;
-            ldsm_x4(RV + swz_offset(8 * n + lane, 2 * k0, pitch), b0, b1, b2, b3);
+            ldsm_x4(RV8(n, k0 / 8), b0, b1, b2, b3);
             mma1688(w.o[n], h0, h1, b0);
             mma1688(w.o[n + 1], h0, h1, b1);
             mma1688(w.o[n + 2], h0, h1, b2);
@@ -237,9 +254,9 @@ __device__ __forceinline__ void dense_unit(RowState<D> &w, uint32_t rows, int se
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int col = 8 * t + 2 * c + (e & 1);
-            s[t][e] = col < (e < 2 ? see0 : see1) ? s[t][e] * scale : -INFINITY;
+            if (col >= (e < 2 ? see0 : see1)) s[t][e] = -INFINITY;
         }
-    fold<NT, D>(w, s);
+    fold<NT, D>(w, s, scale);
     const uint32_t V = rows + UR * D * 2;
 #pragma unroll
     for (int k = 0; k < UR / 16; ++k) {
@@ -249,17 +266,18 @@ __device__ __forceinline__ void dense_unit(RowState<D> &w, uint32_t rows, int se
         auto keep = [&](int t) { return (t < valid ? 0xffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u); };
         const uint32_t k0 = keep(16 * k + 2 * c), k1 = keep(16 * k + 8 + 2 * c);
 #pragma unroll
-        for (int n = 0; n < D / 8; n += 2) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(V + swz_offset(16 * k + (lane & 15), 16 * n + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
-            b0 &= k0;
-            b1 &= k1;
-            b2 &= k0;
-            b3 &= k1;
-            mma16816(w.o[n], hi[0], hi[1], hi[2], hi[3], b0, b1);
-            mma16816(w.o[n + 1], hi[0], hi[1], hi[2], hi[3], b2, b3);
-            mma16816(w.o[n], lo[0], lo[1], lo[2], lo[3], b0, b1);
-            mma16816(w.o[n + 1], lo[0], lo[1], lo[2], lo[3], b2, b3);
+        for (int n0 = 0; n0 < D / 8; n0 += 8) {
+            uint32_t b[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                ldsm_x4_t(V + swz_offset(16 * k + (lane & 15), 16 * (n0 + 2 * n) + 16 * (lane >> 4), D * 2), b[n][0], b[n][1],
+                          b[n][2], b[n][3]);
+                b[n][0] &= k0;
+                b[n][1] &= k1;
+                b[n][2] &= k0;
+                b[n][3] &= k1;
+            }
+            both<8>(w.o + n0, hi, lo, b);
         }
     }
 }
@@ -322,6 +340,10 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
     const int slot0 = pg * SPG;
     const bool active = pg < PG, leader = active && rt == 0 && lane == 0;
     auto slot_of = [&](int k) { return slot0 + k % SPG; };
+    const char *records = p.factor_pool + y.record_offset(p.layer, b, h, 0);
+    const char *dense = p.dense_pool + y.dense_offset(p.layer, b, 0, h, 0);
+    const uint32_t rec_bytes = (uint32_t)y.rec_bytes;
+    const size_t slot_bytes = (size_t)y.H * 2 * y.dense_half_bytes;
     // Leader: the group's k-th unit into its slot.
     auto issue = [&](int k) {
         const int u = pg + k * PG;
@@ -332,10 +354,10 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
         unit(u, page, row);
         unsigned char *dst = sm + (size_t)sl * p.unit_bytes;
         if (row < 0) {
-            mbar_arrive_expect_tx(&sh.full[sl], (uint32_t)y.rec_bytes);
-            bulk_g2s(dst, p.factor_pool + y.record_offset(p.layer, b, h, page), (uint32_t)y.rec_bytes, &sh.full[sl]);
+            mbar_arrive_expect_tx(&sh.full[sl], rec_bytes);
+            bulk_g2s(dst, records + (size_t)page * rec_bytes, rec_bytes, &sh.full[sl]);
         } else {
-            const char *src = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(page), h, 0) + (size_t)row * D * 2;
+            const char *src = dense + y.dense_slot(page) * slot_bytes + (size_t)row * D * 2;
             mbar_arrive_expect_tx(&sh.full[sl], 2 * HALF);
             bulk_g2s(dst, src, HALF, &sh.full[sl]);
             bulk_g2s(dst + HALF, src + y.dense_half_bytes, HALF, &sh.full[sl]);
@@ -349,28 +371,42 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
     // the chunk's rows, swizzled, zeros past the last: units of UR rows
     unsigned char *chunk = sm + (size_t)p.slots * p.unit_bytes;
     const int cu = sp == ns - 1 ? (n + UR - 1) / UR : 0;
-    for (int e = tid; e < cu * UR * 2 * (D / 8); e += blockDim.x) {
-        const int ch = e % (D / 8), kv = e / (D / 8) % 2, t = e / (D / 4), u = t / UR, r = t % UR;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (t < n) v = reinterpret_cast<const uint4 *>((kv ? p.v_new : p.k_new) + ((size_t)(p.off[i] + t) * y.H + h) * (D * 2))[ch];
-        *reinterpret_cast<uint4 *>(chunk + (size_t)u * 2 * HALF + kv * HALF + swz_offset(r, 16 * ch, D * 2)) = v;
+    constexpr int CH = D / 8, AHEAD = 8;  // 16-byte chunks of a row; loads in flight
+    for (int e0 = tid; e0 < cu * UR * 2 * CH; e0 += AHEAD * 32 * SMALL_WARPS) {
+        uint4 v[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int e = e0 + a * 32 * SMALL_WARPS, ch = e % CH, kv = e / CH % 2, t = e / (2 * CH);
+            v[a] = make_uint4(0, 0, 0, 0);
+            if (t < n) v[a] = reinterpret_cast<const uint4 *>((kv ? p.v_new : p.k_new) + ((size_t)(p.off[i] + t) * y.H + h) * (D * 2))[ch];
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int e = e0 + a * 32 * SMALL_WARPS, ch = e % CH, kv = e / CH % 2, t = e / (2 * CH);
+            if (t < cu * UR)
+                *reinterpret_cast<uint4 *>(chunk + (size_t)(t / UR) * 2 * HALF + kv * HALF + swz_offset(t % UR, 16 * ch, D * 2)) = v[a];
+        }
     }
     // the warp's query rows
     RowState<D> w;
     const int r0 = 16 * rt + g;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k)
+    for (int a = 0; a < 2; ++a) {
+        const int r = r0 + 8 * a, tok = r / G;
+        const bool in = active && r < R;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.q) +
+                              (((size_t)(p.off[i] + (in ? tok : 0)) * y.Hq + h * G + (in ? r - tok * G : 0)) * D) / 2 + c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = r0 + 8 * (e & 1), col = 16 * k + 2 * c + 8 * (e >> 1);
-            w.q[k][e] = r < R ? *reinterpret_cast<const uint32_t *>(
-                                    p.q + ((((size_t)(p.off[i] + r / G) * y.Hq + h * G + r % G) * D) + col) * 2)
-                              : 0u;
+        for (int k = 0; k < D / 16; ++k) {
+            w.q[k][a] = in ? src[8 * k] : 0u;
+            w.q[k][2 + a] = in ? src[8 * k + 4] : 0u;
         }
+    }
 #pragma unroll
     for (int t = 0; t < D / 8; ++t) w.o[t][0] = w.o[t][1] = w.o[t][2] = w.o[t][3] = 0.f;
     w.m[0] = w.m[1] = -INFINITY;
     w.l[0] = w.l[1] = 0.f;
+    grid_launch_dependents();  // the merge may be set up
     if (cu) __syncthreads();  // the chunk is in place (the same in every thread)
     if (active) {
         for (int u = pg; u < cu; u += PG)
@@ -381,6 +417,8 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
             // a warp leaves as one
             ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[sl], (k / SPG) & 1, p.status)) != 0;
             if (!ok) break;
+            // the slot of the unit before is free, or nearly: the next copy goes there
+            if (leader && k > 0 && (ok = issue(issued))) ++issued;
             int page, row;
             unit(pg + k * PG, page, row);
             const uint32_t at = smem_u32(sm + (size_t)sl * p.unit_bytes);
@@ -390,13 +428,8 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
                 const int valid = min(UR, T - page * P - row);
                 dense_unit<UR, D>(w, at, valid, valid, valid, p.scale_log2, lane);
             }
-            fence_proxy_async_shared();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[sl]);
-            if (leader) {
-                ok = issue(issued);
-                if (ok) ++issued;
-            }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
         }
