@@ -99,6 +99,7 @@ void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
     rp.y = s->y;
     rp.factor_pool = s->factor_pool;
     rp.dense_pool = s->dense_pool;
+    rp.status = reinterpret_cast<int *>(s->workspace);
     rp.rope_base = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_base_offset);
     rp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_delta_offset);
     rp.layer = layer;
@@ -550,6 +551,7 @@ puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int
                             starts[i], counts[i], T);
             rp.seqs[i] = seq_ids[i];
             lens[i] = rp.T[i] = T;
+            rp.fw[i] = first_window_page(y, T);
             rp.lo[i] = starts[i];
             rp.n[i] = counts[i];
             rp.off[i] = off;
@@ -564,7 +566,7 @@ puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
         wait_conversions(s, strm, seq_ids, lens, B);
         s->after_decode = false;
-        const cudaError_t e = launch_rows(rp, strm);
+        const cudaError_t e = launch_read(rp, s->num_sms, strm);
         if (e != cudaSuccess) return cuda_fail(e, "row read launch");
         return PUZZLEKV_OK;
     });

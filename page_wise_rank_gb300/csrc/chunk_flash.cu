@@ -7,6 +7,7 @@
 #include <algorithm>
 
 #include "kernels.h"
+#include "rebuild.cuh"
 #include "tcgen05.cuh"
 
 namespace pkv {
@@ -161,14 +162,6 @@ struct StageItem {
     }
 };
 
-// Bytes of a page's place in a fetch buffer: the larger factor part of a record,
-// or the page's dense rows.
-__host__ __device__ inline uint32_t stage_page_bytes(const Layout &y) {
-    const size_t kpart = y.off_LV, vpart = y.rec_bytes - y.off_LV, part = kpart > vpart ? kpart : vpart;
-    return (uint32_t)(part > y.dense_half_bytes ? part : y.dense_half_bytes);
-}
-constexpr int STAGE_THREADS = 512;
-
 template <int P, int D>
 __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StageParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
@@ -178,7 +171,6 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
     const Layout &y = p.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int items = 2 * p.blk_off[p.nseq] * y.H;
-    const uint32_t kpart = (uint32_t)y.off_LV, vpart = (uint32_t)(y.rec_bytes - y.off_LV);  // each one stretch of a record
     const uint32_t page_bytes = stage_page_bytes(y);
     unsigned char *img = sm;
     if (tid == 0) {
@@ -187,18 +179,11 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         fence_barrier_init();
     }
     __syncthreads();
-    // factorized pages of an item: [first, last) of its NP pages
-    auto first = [&](const StageItem &it) { return max(0, min(NP, y.sink_pages - it.blk * NP)); };
-    auto last = [&](const StageItem &it) { return max(0, min(NP, it.fw - it.blk * NP)); };
-    auto fetch = [&](int item, int buf) {  // thread 0: the factors of an item
+    auto buffer = [&](int buf) { return sm + IMG + buf * NP * page_bytes; };
+    auto fetch = [&](int item, int buf) {  // one thread: the factors of an item
         const StageItem it(p, item);
-        const int s0 = first(it), s1 = last(it);
-        if (s0 >= s1) return;
-        const uint32_t part = it.kv ? vpart : kpart;
-        mbar_arrive_expect_tx(&bars[buf], (uint32_t)(s1 - s0) * part);
-        const char *src = p.factor_pool + y.record_offset(p.layer, it.b, it.h, it.blk * NP + s0) + (it.kv ? kpart : 0u);
-        for (int s = s0; s < s1; ++s, src += y.rec_bytes)
-            bulk_g2s(sm + IMG + (buf * NP + s) * page_bytes, src, part, &bars[buf]);
+        BlockPages(y, NP, it.blk * NP, it.fw, it.kv)
+            .fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     grid_launch_dependents();  // the attention may be set up
@@ -208,48 +193,22 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         const int next = item + gridDim.x;
         if (tid == 0 && next < items) fetch(next, buf ^ 1);
         const StageItem it(p, item);
-        const int s_lo = first(it), s_hi = last(it), pg0 = it.blk * NP;
-        unsigned char *recs = sm + IMG + buf * NP * page_bytes;
-        // dense pages, the chunk's rows and zeros past the end, in the dense
-        // pages' swizzled rows
-        if (s_lo > 0 || s_hi < NP || s_lo >= s_hi) {
-            const char *chunk = it.kv ? p.v_new : p.k_new;
-            constexpr int CH = D / 8;  // 16-byte chunks of a row
-            constexpr int PER = FLASH_KEYS * CH / STAGE_THREADS;
-            uint4 v[PER];
-            int slot = -1;
-            const char *page = nullptr;
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, s = row / P, pos = pg0 * P + row;
-                v[k] = make_uint4(0, 0, 0, 0);
-                if ((s >= s_lo && s < s_hi) || pos >= it.T1) continue;
-                if (pos >= it.T0) {
-                    v[k] = reinterpret_cast<const uint4 *>(chunk + ((size_t)(p.off[it.i] + pos - it.T0) * y.H + it.h) * (D * 2))[ch];
-                } else {
-                    if (s != slot) {
-                        slot = s;
-                        page = p.dense_pool + y.dense_offset(p.layer, it.b, y.dense_slot(pg0 + s), it.h, it.kv);
-                    }
-                    v[k] = *reinterpret_cast<const uint4 *>(page + swz_offset(row % P, 16 * ch, D * 2));
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < PER; ++k) {
-                const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, s = row / P;
-                if (s >= s_lo && s < s_hi) continue;
-                *reinterpret_cast<uint4 *>(recs + s * page_bytes + swz_offset(row % P, 16 * ch, D * 2)) = v[k];
-            }
+        const BlockPages bp(y, NP, it.blk * NP, it.fw, it.kv);
+        unsigned char *pages = buffer(buf);
+        if (bp.lo > 0 || bp.hi < NP) {
+            fetch_dense<P, D>(y, bp, p.dense_pool, it.kv ? p.v_new : p.k_new, p.off[it.i], p.layer, it.b, it.h, it.kv, it.T0,
+                              it.T1, pages, page_bytes);
             __syncthreads();
         }
-        if (s_lo < s_hi) {
+        if (bp.lo < bp.hi) {
             const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
             if (!ok) {  // let the copies land, then leave the images as they are
                 if (tid == 0) {
                     mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
                     if (next < items) {
                         const StageItem nx(p, next);
-                        if (first(nx) < last(nx)) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
+                        const BlockPages nb(y, NP, nx.blk * NP, nx.fw, nx.kv);
+                        if (nb.lo < nb.hi) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
                     }
                 }
                 break;
@@ -272,85 +231,26 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
             m = lane < STAGE_THREADS / 32 ? red[lane] : 0.f;
             return warp_max(m);
         };
-        auto put = [&](uint32_t r0, uint32_t r1, float *d) {  // a bf16 pair of row g, and of row g + 8
-            d[0] = bf16_lo_to_f32(r0);
-            d[1] = bf16_hi_to_f32(r0);
-            d[2] = bf16_lo_to_f32(r1);
-            d[3] = bf16_hi_to_f32(r1);
-        };
         int scale;  // the image's power of two
         if (it.kv == 0) {
-            // warp: positions 16 w .. 16 w + 15 and half of the columns, tile j
-            // = columns 8 nt(j) .. + 7; column pairs that RoPE turns stay together
-            constexpr int KT = D / 16;
-            const int w = warp & 7, half = warp >> 3, s = 16 * w / P, t0 = 16 * w % P, pg = pg0 + s;
-            auto nt = [&](int j) { return j % (KT / 2) + KT / 2 * half + KT * (j / (KT / 2)); };
+            const RowTile<P, D> rt;
+            constexpr int KT = RowTile<P, D>::KT;
 #pragma unroll
             for (int j = 0; j < KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            const uint32_t base = smem_u32(recs + s * page_bytes);
-            if (s >= s_lo && s < s_hi) {
-                const uint32_t RK = base + (uint32_t)y.off_RK;
-                const int pitch = y.rkp * 2;
-                int k0 = 0;
-                for (; k0 + 16 <= y.rkp; k0 += 16) {
-                    uint32_t a0, a1, a2, a3;
-                    ldsm_x4(base + swz_offset(t0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
-#pragma unroll
-                    for (int j = 0; j < KT; j += 2) {
-                        uint32_t b0, b1, b2, b3;
-                        ldsm_x4_t(RK + swz_offset(k0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
-                        mma16816(acc[j], a0, a1, a2, a3, b0, b1);
-                        mma16816(acc[j + 1], a0, a1, a2, a3, b2, b3);
-                    }
-                }
-                if (k0 < y.rkp) {  // eight ranks left
-                    uint32_t a0, a1;
-                    ldsm_x2(base + swz_offset(t0 + (lane & 15), 2 * k0, pitch), a0, a1);
-#pragma unroll
-                    for (int j = 0; j < KT; j += 2) {
-                        uint32_t b0, b1;
-                        ldsm_x2_t(RK + swz_offset(k0 + (lane & 7), 16 * nt(j) + 16 * ((lane >> 3) & 1), D * 2), b0, b1);
-                        mma1688(acc[j], a0, a1, b0);
-                        mma1688(acc[j + 1], a0, a1, b1);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < KT; j += 2) {
-                    uint32_t r0, r1, r2, r3;
-                    ldsm_x4(base + swz_offset(t0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), r0, r1, r2, r3);
-                    put(r0, r1, acc[j]);
-                    put(r2, r3, acc[j + 1]);
-                }
-            }
-            if (y.rope) {  // turn each pair of columns (i, i + d/2) by its position
-#pragma unroll
-                for (int r2 = 0; r2 < 2; ++r2) {
-                    const int t = t0 + g + 8 * r2;
-                    if (pg * P + t >= it.T1) continue;
-#pragma unroll
-                    for (int j = 0; j < KT / 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = 8 * nt(j) + 2 * c + e;
-                            const float2 a = p.rope_base[(size_t)pg * (D / 2) + i], o = p.rope_delta[t * (D / 2) + i];
-                            const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
-                            float &x0 = acc[j][2 * r2 + e], &x1 = acc[j + KT / 2][2 * r2 + e];
-                            const float u0 = x0 * cs - x1 * sn, u1 = x1 * cs + x0 * sn;
-                            x0 = u0;
-                            x1 = u1;
-                        }
-                }
-            }
+            const uint32_t base = smem_u32(pages + rt.s * page_bytes);
+            if (rt.s >= bp.lo && rt.s < bp.hi)
+                rt.template product<false>(acc, y, base);
+            else
+                rt.rows(acc, base);
+            if (y.rope) rt.turn(acc, p.rope_base, p.rope_delta, bp.pg0 + rt.s, it.T1);
             scale = fp16_exponent(block_max(KT));
             const float f = pow2i(-scale);
 #pragma unroll
             for (int j = 0; j < KT; ++j)
 #pragma unroll
                 for (int r2 = 0; r2 < 2; ++r2) {
-                    const int r = 16 * w + g + 8 * r2;
-                    *reinterpret_cast<uint32_t *>(img + (nt(j) / 8) * (FLASH_KEYS * 128) + r * 128 +
-                                                  (((nt(j) & 7) ^ (r & 7)) << 4) + 4 * c) =
+                    const int r = 16 * rt.w + g + 8 * r2, nt = rt.nt(j);
+                    *reinterpret_cast<uint32_t *>(img + (nt / 8) * (FLASH_KEYS * 128) + r * 128 + (((nt & 7) ^ (r & 7)) << 4) + 4 * c) =
                         pack_f16(acc[j][2 * r2] * f, acc[j][2 * r2 + 1] * f);
                 }
         } else {
@@ -362,8 +262,8 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
 #pragma unroll
             for (int s2 = 0; s2 < KR / PK; ++s2) {
                 const int s = (key0 + s2 * PK) / P, off = (key0 + s2 * PK) % P;  // page, its first position here
-                const uint32_t base = smem_u32(recs + s * page_bytes);
-                if (s >= s_lo && s < s_hi) {
+                const uint32_t base = smem_u32(pages + s * page_bytes);
+                if (s >= bp.lo && s < bp.hi) {
                     const uint32_t RV = base + (uint32_t)(y.off_RV - y.off_LV);
                     const int pitch = y.rvp * 2;
                     int k0 = 0;
@@ -395,8 +295,8 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                         uint32_t r0, r1, r2, r3;
                         ldsm_x4_t(base + swz_offset(off + 8 * j + (lane & 7) + 8 * (lane >> 4), 2 * d0 + 16 * ((lane >> 3) & 1), D * 2),
                                   r0, r1, r2, r3);
-                        put(r0, r1, acc[s2 * PT + j]);
-                        put(r2, r3, acc[s2 * PT + j + 1]);
+                        put_pairs(r0, r1, acc[s2 * PT + j]);
+                        put_pairs(r2, r3, acc[s2 * PT + j + 1]);
                     }
                 }
             }

@@ -114,10 +114,12 @@ struct RowsParams {
     const float2 *rope_base, *rope_delta;
     const char *k_new, *v_new;
     char *k_out, *v_out;
+    int *status;
     size_t row_stride, head_stride;  // elements
     int layer, nseq, turn;
     int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], lo[MAX_CALL_BATCH], n[MAX_CALL_BATCH];
     int off[MAX_CALL_BATCH], coff[MAX_CALL_BATCH];
+    int fw[MAX_CALL_BATCH];  // launch_read: page after the last factorized one
     int page_off[MAX_CALL_BATCH + 1];  // pages touched by the entries before (filled by the launcher)
 };
 
@@ -271,6 +273,8 @@ cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st);
 
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st);
+// launch_rows for rows of the cache alone (no chunk rows).
+cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_append_chunk(const AppendChunkParams &p, cudaStream_t st);
 cudaError_t launch_truncate(const TruncateParams &p, cudaStream_t st);
 cudaError_t launch_load_factors(const LoadFactorsParams &p, cudaStream_t st);

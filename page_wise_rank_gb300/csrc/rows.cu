@@ -2,8 +2,11 @@
 // appending a chunk of tokens, and placing plain factors in a store's records
 // ("PuzzleKV: Page-Wise Low-Rank Decomposition for KV Cache Compression",
 // §3.3 ③-⑤).  Page kinds follow page_kind() in layout.h.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "rebuild.cuh"
 
 namespace pkv {
 
@@ -61,7 +64,7 @@ __device__ void load_page_factors(const Layout &y, const char *rec, int kv, floa
 // RoPE turns together.
 template <typename T>
 __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
-    extern __shared__ __align__(16) float sm[];
+    extern __shared__ __align__(128) unsigned char sm[];
     const Layout &y = p.y;
     const int P = y.P, d = y.d, h = blockIdx.y, kv = blockIdx.z;
     int i = 0;
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
     const bool cached = pg * P < T0;
     const bool factored = cached && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
     const int rp = kv == 0 ? y.rkp : y.rvp;
-    float *Ls = sm, *Rs = sm + P * rp;
+    float *Ls = reinterpret_cast<float *>(sm), *Rs = Ls + P * rp;
     const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, kv);
     if (factored) {
         load_page_factors<T>(y, p.factor_pool + y.record_offset(p.layer, b, h, pg), kv, Ls, Rs);
@@ -118,6 +121,113 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
         T *dst = out + (size_t)(p.off[i] + r - lo) * p.row_stride + (size_t)h * p.head_stride;
         dst[c] = x0;
         dst[c + half] = x1;
+    }
+}
+
+// The same for bf16 factors (no chunk rows), HBM-bound: a factorized row is 0.47
+// of its bytes as factors, and all of them are written.  CTAs stay and loop over
+// items (128 positions of an entry, head, K/V): the next item's factors arrive
+// while one is computed on the warps' tensor cores (fp32 sums, rounded once) and
+// written a whole row per sixteen lanes.  32K tokens x 8 heads, ranks 16 and 24:
+// 0.28 ms with the scalar products of rows_kernel.
+template <int P, int D>
+__global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams p) {
+    extern __shared__ __align__(128) unsigned char sm[];
+    __shared__ uint64_t bars[2];
+    constexpr int NP = BLOCK / P, TILE = BLOCK * D * 2, CH = D / 8;
+    const Layout &y = p.y;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int items = 2 * p.page_off[p.nseq] * y.H;  // page_off: blocks here
+    const uint32_t page_bytes = stage_page_bytes(y);
+    struct Item {
+        int i, b, h, kv, blk, pg0;
+        __device__ __forceinline__ Item(const RowsParams &p, int item) {
+            kv = item & 1;
+            h = (item >> 1) % p.y.H;
+            blk = (item >> 1) / p.y.H;
+            i = 0;
+            while (blk >= p.page_off[i + 1]) ++i;
+            blk -= p.page_off[i];
+            pg0 = p.lo[i] / P + blk * NP;
+            b = p.seqs[i];
+        }
+    };
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    auto buffer = [&](int buf) { return sm + TILE + buf * NP * page_bytes; };
+    // factorized pages of an item that hold asked rows
+    auto wanted = [&](const Item &it) {
+        BlockPages bp(y, NP, it.pg0, p.fw[it.i], it.kv);
+        bp.hi = max(bp.lo, min(bp.hi, (p.lo[it.i] + p.n[it.i] + P - 1) / P - it.pg0));
+        return bp;
+    };
+    auto fetch = [&](int item, int buf) {
+        const Item it(p, item);
+        wanted(it).fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
+    };
+    if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
+    uint32_t phase = 0;
+    int buf = 0;
+    const RowTile<P, D> rt;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
+        const int next = item + gridDim.x;
+        if (tid == 0 && next < items) fetch(next, buf ^ 1);
+        const Item it(p, item);
+        const int i = it.i, lo = p.lo[i], hi = lo + p.n[i];
+        const BlockPages bp = wanted(it);
+        unsigned char *pages = buffer(buf);
+        if (bp.lo > 0 || bp.hi < NP) {
+            // rows past the asked ones are not read: pages of this block past
+            // `hi` may be factorized and have no dense rows
+            fetch_dense<P, D>(y, bp, p.dense_pool, nullptr, 0, p.layer, it.b, it.h, it.kv, hi, hi, pages, page_bytes);
+            __syncthreads();
+        }
+        if (bp.lo < bp.hi) {
+            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
+            if (!ok) {
+                if (tid == 0) {
+                    mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
+                    if (next < items) {
+                        const BlockPages nb = wanted(Item(p, next));
+                        if (nb.lo < nb.hi) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
+                    }
+                }
+                break;
+            }
+            phase ^= 1u << buf;
+        }
+        float acc[8][4];
+#pragma unroll
+        for (int j = 0; j < rt.KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        const uint32_t base = smem_u32(pages + rt.s * page_bytes);
+        if (rt.s < bp.lo || rt.s >= bp.hi)
+            rt.rows(acc, base);
+        else if (it.kv)
+            rt.template product<true>(acc, y, base);
+        else
+            rt.template product<false>(acc, y, base);
+        if (y.rope && it.kv == 0) rt.turn(acc, p.rope_base, p.rope_delta, it.pg0 + rt.s, hi);
+#pragma unroll
+        for (int j = 0; j < rt.KT; ++j)
+#pragma unroll
+            for (int r2 = 0; r2 < 2; ++r2)
+                *reinterpret_cast<uint32_t *>(sm + swz_offset(16 * rt.w + g + 8 * r2, 16 * rt.nt(j) + 4 * c, D * 2)) =
+                    pack_bf16(acc[j][2 * r2], acc[j][2 * r2 + 1]);
+        fence_proxy_async_shared();  // the fetch buffer is read
+        __syncthreads();
+        __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(it.kv ? p.v_out : p.k_out) + (size_t)it.h * p.head_stride;
+#pragma unroll
+        for (int k = 0; k < BLOCK * CH / STAGE_THREADS; ++k) {
+            const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, pos = it.pg0 * P + row;
+            if (pos >= lo && pos < hi)
+                reinterpret_cast<uint4 *>(out + (size_t)(p.off[i] + pos - lo) * p.row_stride)[ch] =
+                    *reinterpret_cast<const uint4 *>(sm + swz_offset(row, 16 * ch, D * 2));
+        }
+        __syncthreads();  // the tile is read
     }
 }
 
@@ -195,6 +305,39 @@ __global__ void load_factors_kernel(const LoadFactorsParams p) {
         const int c = e / y.rvp, j = e % y.rvp;
         *swz_ptr<T>(rec + y.off_RV, c, j, y.rvp) = j < y.rv ? RV[j * d + c] : zero;
     }
+}
+
+template <int P, int D>
+static cudaError_t read_t(const RowsParams &p, int num_sms, cudaStream_t st) {
+    const int smem = BLOCK * D * 2 + 2 * BLOCK / P * (int)stage_page_bytes(p.y);
+    auto k = read_kernel<P, D>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    const int items = 2 * p.page_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
+    k<<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st) {
+    const Layout &y = p.y;
+    if (y.dtype != 1 || y.q4) return launch_rows(p, st);
+    const int np = BLOCK / y.P;
+    p.page_off[0] = 0;
+    for (int i = 0; i < p.nseq; ++i) {
+        const int pages = p.n[i] > 0 ? (p.lo[i] + p.n[i] - 1) / y.P - p.lo[i] / y.P + 1 : 0;
+        p.page_off[i + 1] = p.page_off[i] + (pages + np - 1) / np;
+    }
+    if (p.page_off[p.nseq] == 0) return cudaSuccess;
+    if (y.d == 64) {
+        if (y.P == 16) return read_t<16, 64>(p, num_sms, st);
+        if (y.P == 32) return read_t<32, 64>(p, num_sms, st);
+        return read_t<64, 64>(p, num_sms, st);
+    }
+    if (y.P == 16) return read_t<16, 128>(p, num_sms, st);
+    if (y.P == 32) return read_t<32, 128>(p, num_sms, st);
+    return read_t<64, 128>(p, num_sms, st);
 }
 
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st) {
