@@ -146,6 +146,7 @@ __device__ __forceinline__ float finite_abs(float x) {
 // computed.
 struct StageItem {
     int i, b, T0, T1, fw, h, blk, kv;
+    StageItem() = default;
     __device__ __forceinline__ StageItem(const StageParams &p, int item) {
         kv = item & 1;
         int u = item >> 1;
@@ -166,6 +167,7 @@ template <int P, int D>
 __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StageParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ uint64_t bars[2];
+    __shared__ StageItem its[2];
     __shared__ float red[STAGE_THREADS / 32];
     constexpr int NP = FLASH_KEYS / P, IMG = FLASH_KEYS * D * 2;
     const Layout &y = p.y;
@@ -180,19 +182,20 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
     }
     __syncthreads();
     auto buffer = [&](int buf) { return sm + IMG + buf * NP * page_bytes; };
-    auto fetch = [&](int item, int buf) {  // one thread: the factors of an item
-        const StageItem it(p, item);
+    auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
+        const StageItem it = its[buf] = StageItem(p, item);
         BlockPages(y, NP, it.blk * NP, it.fw, it.kv)
             .fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     grid_launch_dependents();  // the attention may be set up
+    __syncthreads();
     uint32_t phase = 0;  // bit of each buffer's barrier
     int buf = 0;
     for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
         const int next = item + gridDim.x;
         if (tid == 0 && next < items) fetch(next, buf ^ 1);
-        const StageItem it(p, item);
+        const StageItem it = its[buf];
         const BlockPages bp(y, NP, it.blk * NP, it.fw, it.kv);
         unsigned char *pages = buffer(buf);
         if (bp.lo > 0 || bp.hi < NP) {
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                 if (tid == 0) {
                     mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
                     if (next < items) {
-                        const StageItem nx(p, next);
+                        const StageItem nx = its[buf ^ 1];
                         const BlockPages nb(y, NP, nx.blk * NP, nx.fw, nx.kv);
                         if (nb.lo < nb.hi) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
                     }
@@ -264,12 +267,11 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                 const int s = (key0 + s2 * PK) / P, off = (key0 + s2 * PK) % P;  // page, its first position here
                 const uint32_t base = smem_u32(pages + s * page_bytes);
                 if (s >= bp.lo && s < bp.hi) {
-                    const uint32_t RV = base + (uint32_t)(y.off_RV - y.off_LV);
-                    const int pitch = y.rvp * 2;
+                    const SwzRows RV(base + (uint32_t)(y.off_RV - y.off_LV), d0 + (lane & 15), y.rvp * 2);
                     int k0 = 0;
                     for (; k0 + 16 <= y.rvp; k0 += 16) {
                         uint32_t a0, a1, a2, a3;
-                        ldsm_x4(RV + swz_offset(d0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+                        ldsm_x4(RV(0, k0 / 8 + (lane >> 4)), a0, a1, a2, a3);
 #pragma unroll
                         for (int j = 0; j < PT; j += 2) {
                             uint32_t b0, b1, b2, b3;
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                     }
                     if (k0 < y.rvp) {
                         uint32_t a0, a1;
-                        ldsm_x2(RV + swz_offset(d0 + (lane & 15), 2 * k0, pitch), a0, a1);
+                        ldsm_x2(RV(0, k0 / 8), a0, a1);
 #pragma unroll
                         for (int j = 0; j < PT; j += 2) {
                             uint32_t b0, b1;

@@ -78,19 +78,6 @@ __device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4], float sc
     }
 }
 
-// Reads of a swizzled matrix whose rows are `pitch` bytes (set at run time):
-// rows a + 8 n of a lane share their chunk permutation, since eight rows are a
-// whole number of its periods, so it is found once.
-struct Rows {
-    uint32_t at;     // the lane's row a
-    int pitch8, x;   // bytes of eight rows; the permutation
-    __device__ __forceinline__ Rows(uint32_t base, int row, int pitch) : at(base + row * pitch), pitch8(8 * pitch) {
-        const int g = gcd8(pitch >> 4);  // a power of two; the period is 8 / g rows
-        x = (((row & 7) * g) >> 3) & (g - 1);
-    }
-    __device__ __forceinline__ uint32_t operator()(int n, int chunk) const { return at + n * pitch8 + ((chunk ^ x) << 4); }
-};
-
 // A operand (high parts and residuals) of two adjacent accumulator tiles.
 __device__ __forceinline__ void split_tiles(const float *t0, const float *t1, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     split_bf16(t0[0], t0[1], hi[0], lo[0]);
@@ -122,7 +109,7 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
     for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
     {
         const uint32_t RK = rec + (uint32_t)y.off_RK;
-        const Rows LK(rec, row8, y.rkp * 2), LK8(rec, lane & 15, y.rkp * 2);
+        const SwzRows LK(rec, row8, y.rkp * 2), LK8(rec, lane & 15, y.rkp * 2);
         int k0 = 0;
 #pragma unroll 1
         for (; k0 + 16 <= y.rkp; k0 += 16) {
@@ -174,7 +161,7 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
 #pragma unroll
     for (int k = 0; k < P / 16; ++k) split_tiles(s[2 * k], s[2 * k + 1], ph[k], pl[k]);
     const uint32_t LV = rec + (uint32_t)y.off_LV;
-    const Rows RV(rec + (uint32_t)y.off_RV, row8, y.rvp * 2), RV8(rec + (uint32_t)y.off_RV, lane, y.rvp * 2);
+    const SwzRows RV(rec + (uint32_t)y.off_RV, row8, y.rvp * 2), RV8(rec + (uint32_t)y.off_RV, lane, y.rvp * 2);
     int k0 = 0;
 #pragma unroll 1
     for (; k0 + 16 <= y.rvp; k0 += 16) {

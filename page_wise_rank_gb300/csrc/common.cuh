@@ -336,4 +336,17 @@ __device__ __forceinline__ const T *swz_ptr(const void *base, int row, int col, 
                                        swz_offset(row, col * (int)sizeof(T), cols * (int)sizeof(T)));
 }
 
+// Reads of a swizzled matrix whose rows are `pitch` bytes (set at run time):
+// rows a + 8 n of a lane share their chunk permutation, since eight rows are a
+// whole number of its periods, so it is found once.
+struct SwzRows {
+    uint32_t at;     // the lane's row a
+    int pitch8, x;   // bytes of eight rows; the permutation
+    __device__ __forceinline__ SwzRows(uint32_t base, int row, int pitch) : at(base + row * pitch), pitch8(8 * pitch) {
+        const int g = gcd8(pitch >> 4);  // a power of two; the period is 8 / g rows
+        x = (((row & 7) * g) >> 3) & (g - 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(int n, int chunk) const { return at + n * pitch8 + ((chunk ^ x) << 4); }
+};
+
 }  // namespace pkv

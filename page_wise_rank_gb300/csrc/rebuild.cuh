@@ -101,18 +101,20 @@ struct RowTile {
     __device__ __forceinline__ void product(float (&acc)[8][4], const Layout &y, uint32_t base) const {
         const int rp = VALUES ? y.rvp : y.rkp, pitch = rp * 2, half8 = (lane >> 3) & 1, row8 = (lane & 7) + 8 * (lane >> 4);
         const uint32_t R = base + (uint32_t)(VALUES ? y.off_RV - y.off_LV : y.off_RK);
+        const SwzRows rows16(VALUES ? R : base, VALUES ? row8 : t0 + (lane & 15), pitch);  // the matrix of run-time pitch
+        const SwzRows rows8(VALUES ? R : base, VALUES ? lane & 15 : t0 + (lane & 15), pitch);
         int k0 = 0;
         for (; k0 + 16 <= rp; k0 += 16) {
             uint32_t a0, a1, a2, a3;
             if (VALUES)
                 ldsm_x4_t(base + swz_offset(k0 + row8, 2 * t0 + 16 * half8, P * 2), a0, a1, a2, a3);
             else
-                ldsm_x4(base + swz_offset(t0 + (lane & 15), 2 * k0 + 16 * (lane >> 4), pitch), a0, a1, a2, a3);
+                ldsm_x4(rows16(0, k0 / 8 + (lane >> 4)), a0, a1, a2, a3);
 #pragma unroll
             for (int j = 0; j < KT; j += 2) {
                 uint32_t b0, b1, b2, b3;
                 if (VALUES)
-                    ldsm_x4(R + swz_offset(8 * nt(j) + row8, 2 * k0 + 16 * half8, pitch), b0, b1, b2, b3);
+                    ldsm_x4(rows16(nt(j), k0 / 8 + half8), b0, b1, b2, b3);
                 else
                     ldsm_x4_t(R + swz_offset(k0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
                 mma16816(acc[j], a0, a1, a2, a3, b0, b1);
@@ -124,12 +126,12 @@ struct RowTile {
             if (VALUES)
                 ldsm_x2_t(base + swz_offset(k0 + (lane & 7), 2 * t0 + 16 * half8, P * 2), a0, a1);
             else
-                ldsm_x2(base + swz_offset(t0 + (lane & 15), 2 * k0, pitch), a0, a1);
+                ldsm_x2(rows8(0, k0 / 8), a0, a1);
 #pragma unroll
             for (int j = 0; j < KT; j += 2) {
                 uint32_t b0, b1;
                 if (VALUES)
-                    ldsm_x2(R + swz_offset(8 * nt(j) + (lane & 15), 2 * k0, pitch), b0, b1);
+                    ldsm_x2(rows8(nt(j), k0 / 8), b0, b1);
                 else
                     ldsm_x2_t(R + swz_offset(k0 + (lane & 7), 16 * nt(j) + 16 * half8, D * 2), b0, b1);
                 mma1688(acc[j], a0, a1, b0);

@@ -130,28 +130,35 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
 // while one is computed on the warps' tensor cores (fp32 sums, rounded once) and
 // written a whole row per sixteen lanes.  32K tokens x 8 heads, ranks 16 and 24:
 // 0.28 ms with the scalar products of rows_kernel.
+struct ReadItem {
+    int i, b, h, kv, pg0, lo, hi, off, fw;
+    ReadItem() = default;
+    __device__ __forceinline__ ReadItem(const RowsParams &p, int item, int pages) {
+        kv = item & 1;
+        h = (item >> 1) % p.y.H;
+        int blk = (item >> 1) / p.y.H;
+        i = 0;
+        while (blk >= p.page_off[i + 1]) ++i;
+        blk -= p.page_off[i];
+        lo = p.lo[i];
+        hi = lo + p.n[i];
+        pg0 = lo / p.y.P + blk * pages;
+        b = p.seqs[i];
+        off = p.off[i];
+        fw = min(p.fw[i], (hi + p.y.P - 1) / p.y.P);  // factorized pages that hold asked rows
+    }
+};
+
 template <int P, int D>
 __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ uint64_t bars[2];
+    __shared__ ReadItem its[2];
     constexpr int NP = BLOCK / P, TILE = BLOCK * D * 2, CH = D / 8;
     const Layout &y = p.y;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int items = 2 * p.page_off[p.nseq] * y.H;  // page_off: blocks here
     const uint32_t page_bytes = stage_page_bytes(y);
-    struct Item {
-        int i, b, h, kv, blk, pg0;
-        __device__ __forceinline__ Item(const RowsParams &p, int item) {
-            kv = item & 1;
-            h = (item >> 1) % p.y.H;
-            blk = (item >> 1) / p.y.H;
-            i = 0;
-            while (blk >= p.page_off[i + 1]) ++i;
-            blk -= p.page_off[i];
-            pg0 = p.lo[i] / P + blk * NP;
-            b = p.seqs[i];
-        }
-    };
     if (tid == 0) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
@@ -159,26 +166,22 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
     }
     __syncthreads();
     auto buffer = [&](int buf) { return sm + TILE + buf * NP * page_bytes; };
-    // factorized pages of an item that hold asked rows
-    auto wanted = [&](const Item &it) {
-        BlockPages bp(y, NP, it.pg0, p.fw[it.i], it.kv);
-        bp.hi = max(bp.lo, min(bp.hi, (p.lo[it.i] + p.n[it.i] + P - 1) / P - it.pg0));
-        return bp;
-    };
-    auto fetch = [&](int item, int buf) {
-        const Item it(p, item);
-        wanted(it).fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
+    auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
+        const ReadItem it = its[buf] = ReadItem(p, item, NP);
+        BlockPages(y, NP, it.pg0, it.fw, it.kv)
+            .fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
+    __syncthreads();
     uint32_t phase = 0;
     int buf = 0;
     const RowTile<P, D> rt;
     for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
         const int next = item + gridDim.x;
         if (tid == 0 && next < items) fetch(next, buf ^ 1);
-        const Item it(p, item);
-        const int i = it.i, lo = p.lo[i], hi = lo + p.n[i];
-        const BlockPages bp = wanted(it);
+        const ReadItem it = its[buf];
+        const int lo = it.lo, hi = it.hi;
+        const BlockPages bp(y, NP, it.pg0, it.fw, it.kv);
         unsigned char *pages = buffer(buf);
         if (bp.lo > 0 || bp.hi < NP) {
             // rows past the asked ones are not read: pages of this block past
@@ -192,7 +195,8 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
                 if (tid == 0) {
                     mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
                     if (next < items) {
-                        const BlockPages nb = wanted(Item(p, next));
+                        const ReadItem nx = its[buf ^ 1];
+                        const BlockPages nb(y, NP, nx.pg0, nx.fw, nx.kv);
                         if (nb.lo < nb.hi) mbar_wait_bounded(&bars[buf ^ 1], (phase >> (buf ^ 1)) & 1, nullptr);
                     }
                 }
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
         for (int k = 0; k < BLOCK * CH / STAGE_THREADS; ++k) {
             const int e = tid + k * STAGE_THREADS, row = e / CH, ch = e % CH, pos = it.pg0 * P + row;
             if (pos >= lo && pos < hi)
-                reinterpret_cast<uint4 *>(out + (size_t)(p.off[i] + pos - lo) * p.row_stride)[ch] =
+                reinterpret_cast<uint4 *>(out + (size_t)(it.off + pos - lo) * p.row_stride)[ch] =
                     *reinterpret_cast<const uint4 *>(sm + swz_offset(row, 16 * ch, D * 2));
         }
         __syncthreads();  // the tile is read
