@@ -384,10 +384,11 @@ class Store:
             raise ValueError("counts must be in [0, max_tokens_per_seq]")
         N = sum(cnt[:B])
         with self._on(stream):
-            k = torch.empty(max(N, 1), c.num_kv_heads, c.head_dim, dtype=c.kv_dtype, device=self.dense_pool.device)
-            v = torch.empty_like(k)
+            # one row at least, so that an empty read still has a pointer
+            kv = torch.empty(2, max(N, 1), c.num_kv_heads, c.head_dim, dtype=c.kv_dtype, device=self.dense_pool.device)
+            k, v = kv.unbind(0)
             check(lib().puzzlekv_read_tokens(self._h, layer, ids, st, cnt, B, _ptr(k), _ptr(v), _stream(stream)))
-        return k[:N], v[:N]
+        return (k, v) if N else (k[:0], v[:0])
 
     def load_factors(self, layer: int, seq: int, page0: int, LK: torch.Tensor, RK: torch.Tensor, LV: torch.Tensor,
                      RV: torch.Tensor, stream=None) -> None:

@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkAttnParams 
 template <typename T, int D>
 static cudaError_t simple_t(ChunkAttnParams &p, cudaStream_t st) {
     constexpr int smem = ((CS_ROWS + 2 * CS_KEYS) * (D + 4) + CS_ROWS * (CS_KEYS + 1)) * 4;
-    cudaError_t e = cudaFuncSetAttribute(chunk_simple_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<chunk_simple_kernel<T, D>>(smem);
     if (e != cudaSuccess) return e;
     chunk_simple_kernel<T, D><<<(unsigned)p.tile_off[p.nseq], 128, smem, st>>>(p);
     return cudaGetLastError();

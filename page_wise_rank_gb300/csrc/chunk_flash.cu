@@ -704,13 +704,10 @@ __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
 template <int P, int D>
 static cudaError_t stage_t(const StageParams &p, int num_sms, cudaStream_t st) {
     const int smem = FLASH_KEYS * D * 2 + 2 * FLASH_KEYS / P * (int)stage_page_bytes(p.y);  // at most 32 + 2 x 41 KB
-    auto k = stage_kernel<P, D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaError_t e = allow_smem<stage_kernel<P, D>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.blk_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    k<<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
+    stage_kernel<P, D><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -729,7 +726,7 @@ cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st) {
 template <int D>
 static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
     constexpr int smem = (2 + RING) * FLASH_KEYS * D * 2 + 1024;
-    cudaError_t e = cudaFuncSetAttribute(flash_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<flash_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(flash_kernel<D>, dim3((unsigned)p.ctas), FLASH_THREADS, smem, st, p);
     if (e != cudaSuccess || p.ctas == 1) return e;

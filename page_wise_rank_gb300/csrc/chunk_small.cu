@@ -494,7 +494,7 @@ size_t small_smem_bytes(const Layout &y, int most_tokens) {
 
 template <int P, int D>
 static cudaError_t small_t(const SmallParams &p, size_t smem, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(small_kernel<P, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem<small_kernel<P, D>>(smem);
     if (e != cudaSuccess) return e;
     small_kernel<P, D><<<dim3((unsigned)(p.boff[p.nseq] - p.nseq), (unsigned)p.y.H), 32 * SMALL_WARPS, smem, st>>>(p);
     return cudaGetLastError();

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "layout.h"
 
 namespace pkv {
@@ -133,6 +135,26 @@ __device__ __forceinline__ void fence_proxy_async_shared() { asm volatile("fence
 // has completed and its memory is visible / let the next grid start early.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Allow `Kernel` `bytes` of dynamic shared memory on the current device, with
+// the largest shared-memory split.  Set again only for more than before: per
+// launch it would cost more host time than a small launch takes on the GPU.
+template <auto Kernel>
+inline cudaError_t allow_smem(size_t bytes) {
+    static std::atomic<int> allowed[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (allowed[dev].load(std::memory_order_acquire) >= (int)bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    int had = allowed[dev].load();
+    while (e == cudaSuccess && had < (int)bytes && !allowed[dev].compare_exchange_weak(had, (int)bytes)) {
+    }
+    return e;
+}
 
 // Launch a kernel that begins with grid_dependency_wait in every block: it may
 // be set up while the launch before it in the stream finishes.

@@ -314,13 +314,10 @@ __global__ void load_factors_kernel(const LoadFactorsParams p) {
 template <int P, int D>
 static cudaError_t read_t(const RowsParams &p, int num_sms, cudaStream_t st) {
     const int smem = BLOCK * D * 2 + 2 * BLOCK / P * (int)stage_page_bytes(p.y);
-    auto k = read_kernel<P, D>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    cudaError_t e = allow_smem<read_kernel<P, D>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.page_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    k<<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
+    read_kernel<P, D><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 

@@ -135,7 +135,7 @@ cudaError_t launch_copy(CopyParams &p, int num_sms, cudaStream_t st) {
     const long total = (long)t.per_layer * p.y.L;
     const long work = total > (long)p.npair * p.y.L ? total : (long)p.npair * p.y.L;
     const int smem = p.tile * p.nsrc;
-    cudaError_t e = cudaFuncSetAttribute(copy_sequences_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, COPY_SMEM);
+    cudaError_t e = allow_smem<copy_sequences_kernel>(COPY_SMEM);
     if (e != cudaSuccess) return e;
     const long most = (long)num_sms * std::min(16, 220 * 1024 / (smem + 1024));
     const long grid = work < most ? work : most;
