@@ -8,6 +8,7 @@ Cache Compression".
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional, Sequence
@@ -176,6 +177,7 @@ class Store:
                                           _ptr(self.page_table), _ptr(self.workspace), _stream(stream),
                                           ctypes.byref(h)))
         self._h = h
+        self._index = self.dense_pool.device.index
 
     def close(self) -> None:
         if getattr(self, "_h", None):
@@ -308,7 +310,13 @@ class Store:
         current one) as torch's current stream, so that what the call allocates belongs to it."""
         if stream is not None:
             return torch.cuda.stream(stream)
-        return torch.cuda.device(self.dense_pool.device)
+        if torch.cuda.current_device() == self._index:
+            return contextlib.nullcontext()
+        return torch.cuda.device(self._index)
+
+    def _queue(self, stream) -> ctypes.c_void_p:
+        s = stream if stream is not None else torch.cuda.current_stream(self._index)
+        return ctypes.c_void_p(s.cuda_stream)
 
     def _need_here(self, t: torch.Tensor, shape, name: str) -> None:
         _need(t, shape, self.cfg.kv_dtype, name)
@@ -351,7 +359,7 @@ class Store:
                 return out
             work = workspace if workspace is not None else self._scratch(nb.value)
             check(lib().puzzlekv_chunk_attention(self._h, layer, _ptr(q), _ptr(k), _ptr(v), _ptr(out), ids, cnt, B,
-                                                 _ptr(work), work.numel() * work.element_size(), _stream(stream)))
+                                                 _ptr(work), work.numel() * work.element_size(), self._queue(stream)))
         return out
 
     def append_chunk(self, layer: int, k: torch.Tensor, v: torch.Tensor, seq_ids: Sequence[int],
@@ -371,7 +379,7 @@ class Store:
                 return
             work = self._scratch(nb.value) if nb.value else None
             check(lib().puzzlekv_append_chunk(self._h, layer, _ptr(k), _ptr(v), ids, cnt, B,
-                                              _ptr(work) if work is not None else None, nb.value, _stream(stream)))
+                                              _ptr(work) if work is not None else None, nb.value, self._queue(stream)))
 
     def read_tokens(self, layer: int, seq_ids: Sequence[int], starts: Sequence[int], counts: Sequence[int],
                     stream=None) -> tuple:
@@ -387,7 +395,7 @@ class Store:
             # one row at least, so that an empty read still has a pointer
             kv = torch.empty(2, max(N, 1), c.num_kv_heads, c.head_dim, dtype=c.kv_dtype, device=self.dense_pool.device)
             k, v = kv.unbind(0)
-            check(lib().puzzlekv_read_tokens(self._h, layer, ids, st, cnt, B, _ptr(k), _ptr(v), _stream(stream)))
+            check(lib().puzzlekv_read_tokens(self._h, layer, ids, st, cnt, B, _ptr(k), _ptr(v), self._queue(stream)))
         return (k, v) if N else (k[:0], v[:0])
 
     def load_factors(self, layer: int, seq: int, page0: int, LK: torch.Tensor, RK: torch.Tensor, LV: torch.Tensor,
@@ -404,7 +412,7 @@ class Store:
         self._need_here(RV, (H, n, c.rank_v, d), "RV")
         with self._on(stream):
             check(lib().puzzlekv_load_factors(self._h, layer, seq, page0, n, _ptr(LK), _ptr(RK), _ptr(LV), _ptr(RV),
-                                              _stream(stream)))
+                                              self._queue(stream)))
 
     def copy_sequences(self, src_ids: Sequence[int], dst_ids: Sequence[int], stream=None) -> None:
         """Slot dst_ids[i] becomes what slot src_ids[i] was before the call, all pairs at once
@@ -412,14 +420,14 @@ class Store:
         n = len(dst_ids)
         with self._on(stream):
             check(lib().puzzlekv_copy_sequences(self._h, _ints(src_ids, n, "src_ids"), _ints(dst_ids, n, "dst_ids"), n,
-                                                _stream(stream)))
+                                                self._queue(stream)))
 
     def truncate_sequences(self, seq_ids: Sequence[int], lengths: Sequence[int], stream=None) -> None:
         """Cut sequences back to lengths[i] tokens in every layer (0 empties the slot); the pages
         that become dense again must still be in the dense ring."""
         ids, B = _seq_ids(seq_ids)
         with self._on(stream):
-            check(lib().puzzlekv_truncate_sequences(self._h, ids, _ints(lengths, B, "lengths"), B, _stream(stream)))
+            check(lib().puzzlekv_truncate_sequences(self._h, ids, _ints(lengths, B, "lengths"), B, self._queue(stream)))
 
     def stats(self, seq: int, layer: int) -> dict:
         n = ctypes.c_int32()

@@ -16,6 +16,12 @@ namespace pkv {
 
 constexpr int CS_ROWS = 32, CS_KEYS = 32;  // query rows and keys of a tile
 
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(bf16_lo_to_f32(v.x), bf16_hi_to_f32(v.x), bf16_lo_to_f32(v.y), bf16_hi_to_f32(v.y));
+}
+
 // Block (tile of 32 query rows of one (entry, KV head), split): 128 threads,
 // eight to a pair of rows.  A thread scores 2 rows x 4 keys and accumulates
 // 2 rows x D/8 columns, so that a shared-memory vector feeds two rows.
@@ -35,10 +41,21 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
     const int Tk = p.T[i] + p.n[i], nkb = (Tk + CS_KEYS - 1) / CS_KEYS;
     const int kb0 = (int)((long long)nkb * sp / ns), kb1 = (int)((long long)nkb * (sp + 1) / ns);
     const T *q = reinterpret_cast<const T *>(p.q);
-    for (int e = tid; e < CS_ROWS * D; e += 128) {
-        const int r = row0 + e / D, c = e % D;
-        Qs[(e / D) * PQ + c] =
-            r < R ? p.scale_log2 * Elem<T>::load(q + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D + c) : 0.f;
+    constexpr int PER = CS_KEYS * D / 4 / 128;  // groups of four elements of a tile per thread
+    {
+        float4 v[PER];
+#pragma unroll
+        for (int a = 0; a < PER; ++a) {
+            const int e = tid + 128 * a, r = row0 + e / (D / 4), tok = r / G;
+            v[a] = r < R ? load4(q + ((size_t)(p.off[i] + tok) * p.Hq + h * G + r - tok * G) * D + e % (D / 4) * 4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int a = 0; a < PER; ++a) {
+            const int e = tid + 128 * a;
+            *reinterpret_cast<float4 *>(Qs + e / (D / 4) * PQ + e % (D / 4) * 4) =
+                make_float4(v[a].x * p.scale_log2, v[a].y * p.scale_log2, v[a].z * p.scale_log2, v[a].w * p.scale_log2);
+        }
     }
     int lim[2];  // last key each of the thread's rows sees (-1: no such row)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][D / 8];
@@ -53,11 +70,20 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
     const T *K = reinterpret_cast<const T *>(p.K) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
     const T *V = reinterpret_cast<const T *>(p.V) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
     for (int kb = kb0; kb < kb1 && kb * CS_KEYS <= last_key; ++kb) {
+        float4 kr[PER], vr[PER];  // in flight together, past the last tile's arithmetic
+#pragma unroll
+        for (int a = 0; a < PER; ++a) {
+            const int e = tid + 128 * a, t = kb * CS_KEYS + e / (D / 4);
+            const size_t at = (size_t)t * p.H * D + e % (D / 4) * 4;
+            kr[a] = t < Tk ? load4(K + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vr[a] = t < Tk ? load4(V + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         __syncthreads();
-        for (int e = tid; e < CS_KEYS * D; e += 128) {
-            const int k = e / D, c = e % D, t = kb * CS_KEYS + k;
-            Ks[k * PQ + c] = t < Tk ? Elem<T>::load(K + (size_t)t * p.H * D + c) : 0.f;
-            Vs[k * PQ + c] = t < Tk ? Elem<T>::load(V + (size_t)t * p.H * D + c) : 0.f;
+#pragma unroll
+        for (int a = 0; a < PER; ++a) {
+            const int e = tid + 128 * a, at = e / (D / 4) * PQ + e % (D / 4) * 4;
+            *reinterpret_cast<float4 *>(Ks + at) = kr[a];
+            *reinterpret_cast<float4 *>(Vs + at) = vr[a];
         }
         __syncthreads();
         float s[2][4] = {};
