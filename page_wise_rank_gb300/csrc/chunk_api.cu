@@ -89,7 +89,7 @@ struct AttnPlan {
     SmallParams s{};                   // bf16 stores: entries of few query rows
     FlashParams f{};                   // bf16 stores: the others (staged as `g`)
     StageParams g{};
-    ChunkAttnParams a{};               // fp32 and INT4 stores, rebuilt by `r`; the merge of split states
+    ChunkAttnParams a{};               // fp32 stores, rebuilt by `r`; the merge of split states
     RowsParams r{};
     size_t images = 0, scales = 0, flash_parts = 0, keys = 0, values = 0, parts = 0, bytes = 0;  // offsets, total
 };
@@ -177,9 +177,9 @@ void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_i
                     AttnPlan &pl) {
     const Layout &y = s->y;
     const float scale = (float)(1.4426950408889634074 / std::sqrt((double)y.d));
-    const bool tensor = y.dtype == 1 && !y.q4;
+    const bool tensor = y.dtype == 1;
     int most_small = 0;
-    if (tensor && !y.rope)
+    if (tensor && !y.rope && !y.q4)
         for (int i = 0; i < B; ++i)
             if (counts[i] <= SMALL_ROWS / y.G) most_small = std::max(most_small, counts[i]);
     const int small_tokens = most_small && small_smem_bytes(y, most_small) ? most_small : 0;

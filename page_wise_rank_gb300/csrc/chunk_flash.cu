@@ -163,7 +163,7 @@ struct StageItem {
     }
 };
 
-template <int P, int D>
+template <int P, int D, bool Q4>
 __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StageParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ uint64_t bars[2];
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
     const Layout &y = p.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int items = 2 * p.blk_off[p.nseq] * y.H;
-    const uint32_t page_bytes = stage_page_bytes(y);
+    const BlockLayout bl(y);
     unsigned char *img = sm;
     if (tid == 0) {
         mbar_init(&bars[0], 1);
@@ -181,11 +181,11 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         fence_barrier_init();
     }
     __syncthreads();
-    auto buffer = [&](int buf) { return sm + IMG + buf * NP * page_bytes; };
+    auto buffer = [&](int buf) { return sm + IMG + buf * NP * bl.fetch_bytes; };
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
         const StageItem it = its[buf] = StageItem(p, item);
         BlockPages(y, NP, it.blk * NP, it.fw, it.kv)
-            .fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
+            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     grid_launch_dependents();  // the attention may be set up
@@ -197,10 +197,10 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         if (tid == 0 && next < items) fetch(next, buf ^ 1);
         const StageItem it = its[buf];
         const BlockPages bp(y, NP, it.blk * NP, it.fw, it.kv);
-        unsigned char *pages = buffer(buf);
+        unsigned char *pages = Q4 ? buffer(2) : buffer(buf);
         if (bp.lo > 0 || bp.hi < NP) {
             fetch_dense<P, D>(y, bp, p.dense_pool, it.kv ? p.v_new : p.k_new, p.off[it.i], p.layer, it.b, it.h, it.kv, it.T0,
-                              it.T1, pages, page_bytes);
+                              it.T1, pages, bl.page_bytes);
             __syncthreads();
         }
         if (bp.lo < bp.hi) {
@@ -217,6 +217,10 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                 break;
             }
             phase ^= 1u << buf;
+            if (Q4) {
+                bp.expand(y, bl, it.kv, buffer(buf), pages);
+                __syncthreads();
+            }
         }
         float acc[8][4];
         // the largest finite |acc| of the CTA; also past the last image's store
@@ -238,13 +242,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         if (it.kv == 0) {
             const RowTile<P, D> rt;
             constexpr int KT = RowTile<P, D>::KT;
-#pragma unroll
-            for (int j = 0; j < KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-            const uint32_t base = smem_u32(pages + rt.s * page_bytes);
-            if (rt.s >= bp.lo && rt.s < bp.hi)
-                rt.template product<false>(acc, y, base);
-            else
-                rt.rows(acc, base);
+            rt.template rebuild<Q4>(acc, y, bl, bp, 0, pages, buffer(buf));
             if (y.rope) rt.turn(acc, p.rope_base, p.rope_delta, bp.pg0 + rt.s, it.T1);
             scale = fp16_exponent(block_max(KT));
             const float f = pow2i(-scale);
@@ -265,9 +263,9 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
 #pragma unroll
             for (int s2 = 0; s2 < KR / PK; ++s2) {
                 const int s = (key0 + s2 * PK) / P, off = (key0 + s2 * PK) % P;  // page, its first position here
-                const uint32_t base = smem_u32(pages + s * page_bytes);
+                const uint32_t base = smem_u32(pages + s * bl.page_bytes);
                 if (s >= bp.lo && s < bp.hi) {
-                    const SwzRows RV(base + (uint32_t)(y.off_RV - y.off_LV), d0 + (lane & 15), y.rvp * 2);
+                    const SwzRows RV(base + bl.vR, d0 + (lane & 15), y.rvp * 2);
                     int k0 = 0;
                     for (; k0 + 16 <= y.rvp; k0 += 16) {
                         uint32_t a0, a1, a2, a3;
@@ -276,8 +274,8 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                         for (int j = 0; j < PT; j += 2) {
                             uint32_t b0, b1, b2, b3;
                             ldsm_x4_t(base + swz_offset(k0 + (lane & 15), 2 * off + 16 * j + 16 * (lane >> 4), P * 2), b0, b1, b2, b3);
-                            mma16816(acc[s2 * PT + j], a0, a1, a2, a3, b0, b1);
-                            mma16816(acc[s2 * PT + j + 1], a0, a1, a2, a3, b2, b3);
+                            Ops<Q4>::mma(acc[s2 * PT + j], a0, a1, a2, a3, b0, b1);
+                            Ops<Q4>::mma(acc[s2 * PT + j + 1], a0, a1, a2, a3, b2, b3);
                         }
                     }
                     if (k0 < y.rvp) {
@@ -287,9 +285,17 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                         for (int j = 0; j < PT; j += 2) {
                             uint32_t b0, b1;
                             ldsm_x2_t(base + swz_offset(k0 + (lane & 7), 2 * off + 16 * j + 16 * ((lane >> 3) & 1), P * 2), b0, b1);
-                            mma1688(acc[s2 * PT + j], a0, a1, b0);
-                            mma1688(acc[s2 * PT + j + 1], a0, a1, b1);
+                            Ops<Q4>::mma8(acc[s2 * PT + j], a0, a1, b0);
+                            Ops<Q4>::mma8(acc[s2 * PT + j + 1], a0, a1, b1);
                         }
+                    }
+                    if (Q4) {
+                        const float dim[2] = {bp.dim_scale(y, bl, buffer(buf), s, 1, d0 + g), bp.dim_scale(y, bl, buffer(buf), s, 1, d0 + g + 8)};
+#pragma unroll
+                        for (int j = 0; j < PT; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[s2 * PT + j][e] *= dim[e >> 1] * bp.token_scale(y, bl, buffer(buf), s, off + 8 * j + 2 * c + (e & 1));
                     }
                 } else {
 #pragma unroll
@@ -701,26 +707,28 @@ __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
     }
 }
 
-template <int P, int D>
+template <int P, int D, bool Q4>
 static cudaError_t stage_t(const StageParams &p, int num_sms, cudaStream_t st) {
-    const int smem = FLASH_KEYS * D * 2 + 2 * FLASH_KEYS / P * (int)stage_page_bytes(p.y);  // at most 32 + 2 x 41 KB
-    cudaError_t e = allow_smem<stage_kernel<P, D>>(smem);
+    const int smem = FLASH_KEYS * D * 2 + (int)BlockLayout(p.y).smem(p.y, FLASH_KEYS / P);  // at most 32 + 2 x 41 KB
+    cudaError_t e = allow_smem<stage_kernel<P, D, Q4>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.blk_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    stage_kernel<P, D><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
+    stage_kernel<P, D, Q4><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st) {
     if (p.blk_off[p.nseq] == 0) return cudaSuccess;
-    if (p.y.d == 64) {
-        if (p.y.P == 16) return stage_t<16, 64>(p, num_sms, st);
-        if (p.y.P == 32) return stage_t<32, 64>(p, num_sms, st);
-        return stage_t<64, 64>(p, num_sms, st);
-    }
-    if (p.y.P == 16) return stage_t<16, 128>(p, num_sms, st);
-    if (p.y.P == 32) return stage_t<32, 128>(p, num_sms, st);
-    return stage_t<64, 128>(p, num_sms, st);
+#define PKV_STAGE_CASE(PP, DD) \
+    if (p.y.P == PP && p.y.d == DD) return p.y.q4 ? stage_t<PP, DD, true>(p, num_sms, st) : stage_t<PP, DD, false>(p, num_sms, st);
+    PKV_STAGE_CASE(16, 64)
+    PKV_STAGE_CASE(32, 64)
+    PKV_STAGE_CASE(64, 64)
+    PKV_STAGE_CASE(16, 128)
+    PKV_STAGE_CASE(32, 128)
+    PKV_STAGE_CASE(64, 128)
+#undef PKV_STAGE_CASE
+    return cudaErrorInvalidValue;
 }
 
 template <int D>

@@ -2,9 +2,13 @@
 // blocks of 128 positions of one KV head, keys or values, as fp32 accumulator
 // tiles.  Shared by the kernels that stage operand images and that read rows.
 //
-// A block's pages lie in a fetch buffer, page s at s * stage_page_bytes: the
-// key (LK, RK) or value (LVt, RVt) part of a factorized page's record, as stored,
-// or a dense page's rows, swizzled as in the dense pool.
+// A block's pages lie in shared memory, page s at s * page_bytes: the key (LK,
+// RK) or value (LVt, RVt) part of a factorized page's record, as stored, or a
+// dense page's rows, swizzled as in the dense pool.  INT4 records arrive in a
+// fetch buffer of their own and are expanded from there to the same matrices in
+// fp16: codes as they are (exact), only L_K's times their rank's scale, whose
+// products need two fp16 (high part and residual) because the scale sits inside
+// the contraction.  The other scales multiply the finished rows.
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
@@ -14,31 +18,94 @@ namespace pkv {
 constexpr int BLOCK = 128;            // positions of a block
 constexpr int STAGE_THREADS = 512;    // two warps to 16 positions
 
-// Bytes of a page's place in a fetch buffer: the larger factor part of a record,
-// or the page's dense rows.
-__host__ __device__ inline uint32_t stage_page_bytes(const Layout &y) {
-    const size_t kpart = y.off_LV, vpart = y.rec_bytes - y.off_LV, part = kpart > vpart ? kpart : vpart;
-    return (uint32_t)(part > y.dense_half_bytes ? part : y.dense_half_bytes);
-}
+// Where a page's matrices lie and how they arrive.
+struct BlockLayout {
+    uint32_t page_bytes;    // a page's place: its larger factor part, or its dense rows
+    uint32_t kR, vR;        // offsets of RK and RVt in it (LK, LVt at 0; INT4: L_K's residuals behind LK)
+    uint32_t fetch_bytes;   // INT4: a page's place in the fetch buffer,
+    uint32_t scales;        // and the offset of its scale vectors there
+    __host__ __device__ explicit BlockLayout(const Layout &y) {
+        const uint32_t lk = (uint32_t)(y.P * y.rkp * 2), rk = (uint32_t)(y.rkp * y.d * 2);
+        const uint32_t lv = (uint32_t)(y.P * y.rvp * 2), rv = (uint32_t)(y.rvp * y.d * 2);
+        kR = y.q4 ? 2 * lk : lk;
+        vR = lv;
+        const uint32_t kpart = kR + rk, vpart = vR + rv, part = kpart > vpart ? kpart : vpart;
+        page_bytes = part > y.dense_half_bytes ? part : (uint32_t)y.dense_half_bytes;
+        const uint32_t ks = (uint32_t)y.q_off_V, vs = (uint32_t)(y.q_off_sRK - y.q_off_V);
+        scales = ks > vs ? ks : vs;
+        fetch_bytes = (scales + (uint32_t)(y.rec_bytes - y.q_off_sRK) + 127) & ~127u;
+        if (!y.q4) fetch_bytes = page_bytes;
+    }
+    // Shared memory for two fetch buffers of `pages` pages (INT4: and the expanded pages).
+    __host__ __device__ uint32_t smem(const Layout &y, int pages) const {
+        return 2 * pages * fetch_bytes + (y.q4 ? pages * page_bytes : 0);
+    }
+};
 
 // A block of `pages` pages from page pg0 on: which of them are factorized, and
 // where their parts lie.
 struct BlockPages {
     int pg0, lo, hi;  // pages [lo, hi) of the block are factorized
-    uint32_t part;    // bytes of one part
     __device__ __forceinline__ BlockPages(const Layout &y, int pages, int pg0_, int fw, int kv) : pg0(pg0_) {
         lo = max(0, min(pages, y.sink_pages - pg0));
         hi = max(0, min(pages, fw - pg0));
         if (hi < lo) hi = lo;
-        part = (uint32_t)(kv ? y.rec_bytes - y.off_LV : y.off_LV);
     }
     // One thread: start the copies of the factorized pages' parts.
-    __device__ __forceinline__ void fetch(const Layout &y, const char *factor_pool, int layer, int b, int h, int kv,
-                                          unsigned char *buf, uint32_t page_bytes, uint64_t *bar) const {
+    template <bool Q4>
+    __device__ __forceinline__ void fetch(const Layout &y, const BlockLayout &bl, const char *factor_pool, int layer, int b, int h,
+                                          int kv, unsigned char *buf, uint64_t *bar) const {
         if (lo == hi) return;
-        mbar_arrive_expect_tx(bar, (uint32_t)(hi - lo) * part);
-        const char *src = factor_pool + y.record_offset(layer, b, h, pg0 + lo) + (kv ? y.off_LV : 0);
-        for (int s = lo; s < hi; ++s, src += y.rec_bytes) bulk_g2s(buf + s * page_bytes, src, part, bar);
+        const size_t off = kv ? (Q4 ? y.q_off_V : y.off_LV) : 0;
+        const uint32_t part = (uint32_t)((kv ? (Q4 ? y.q_off_sRK : y.rec_bytes) : (Q4 ? y.q_off_V : y.off_LV)) - off);
+        const uint32_t tail = Q4 ? (uint32_t)(y.rec_bytes - y.q_off_sRK) : 0;
+        mbar_arrive_expect_tx(bar, (uint32_t)(hi - lo) * (part + tail));
+        const char *src = factor_pool + y.record_offset(layer, b, h, pg0 + lo);
+        for (int s = lo; s < hi; ++s, src += y.rec_bytes) {
+            bulk_g2s(buf + s * bl.fetch_bytes, src + off, part, bar);
+            if (Q4) bulk_g2s(buf + s * bl.fetch_bytes + bl.scales, src + y.q_off_sRK, tail, bar);
+        }
+    }
+    // INT4: the factorized pages' matrices from their codes.  All threads; a barrier follows.
+    __device__ __forceinline__ void expand(const Layout &y, const BlockLayout &bl, int kv, const unsigned char *buf,
+                                           unsigned char *pages) const {
+        const int K1 = kv ? y.P : y.d, r = kv ? y.rvp : y.rkp, K2 = r, N2 = kv ? y.d : y.P;
+        const int n1 = q4_operand_regs(K1, r), n = n1 + q4_operand_regs(K2, N2);
+        for (int e = threadIdx.x; e < (hi - lo) * n * 32; e += blockDim.x) {
+            const int s = lo + e / (n * 32), m = e / 32 % n, lane = e % 32, w = m / 4;
+            const unsigned char *src = buf + s * bl.fetch_bytes;
+            unsigned char *dst = pages + s * bl.page_bytes;
+            const uint32_t word = *reinterpret_cast<const uint32_t *>(src + ((w / 2) * 32 + lane) * 8 + (w % 2) * 4);
+            // nibbles m % 4 and m % 4 + 4: elements (k, n) and (k + 1, n)
+            const float c0 = (float)((int)((word >> (4 * (m % 4))) & 15u) - 8), c1 = (float)((int)((word >> (4 * (m % 4) + 16)) & 15u) - 8);
+            int k, col;
+            if (m < n1) {  // R_K [dim][rank] -> RK[rank][dim];  L_V [token][rank] -> LVt[rank][token]
+                q4_operand_elem(K1, r, m, lane, 0, k, col);
+                *reinterpret_cast<uint32_t *>(dst + (kv ? 0u : bl.kR) + swz_offset(col, 2 * k, K1 * 2)) = pack_f16(c0, c1);
+            } else {  // L_K [rank][token] -> LK[token][rank];  R_V [rank][dim] -> RVt[dim][rank]
+                q4_operand_elem(K2, N2, m - n1, lane, 0, k, col);
+                const uint32_t at = swz_offset(col, 2 * k, r * 2);
+                if (kv) {
+                    *reinterpret_cast<uint32_t *>(dst + bl.vR + at) = pack_f16(c0, c1);
+                } else {
+                    const __half *sLK = reinterpret_cast<const __half *>(src + bl.scales + (y.q_off_sLK - y.q_off_sRK));
+                    uint32_t hi16, lo16;
+                    split_f16(c0 * __half2float(sLK[q4_scale_index(r, k)]), c1 * __half2float(sLK[q4_scale_index(r, k + 1)]), hi16,
+                              lo16);
+                    *reinterpret_cast<uint32_t *>(dst + at) = hi16;
+                    *reinterpret_cast<uint32_t *>(dst + y.P * r * 2 + at) = lo16;
+                }
+            }
+        }
+    }
+    // INT4: scales of page s: s_RK or s_RV of a head dimension, s_LV of a token.
+    __device__ __forceinline__ float dim_scale(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int kv, int dim) const {
+        const unsigned char *at = buf + s * bl.fetch_bytes + bl.scales + (kv ? y.q_off_sRV - y.q_off_sRK : 0);
+        return __half2float(reinterpret_cast<const __half *>(at)[q4_dscale_index(dim)]);
+    }
+    __device__ __forceinline__ float token_scale(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int t) const {
+        const unsigned char *at = buf + s * bl.fetch_bytes + bl.scales + (y.q_off_sLV - y.q_off_sRK);
+        return __half2float(reinterpret_cast<const __half *>(at)[q4_scale_index(y.P, t)]);
     }
 };
 
@@ -95,12 +162,10 @@ struct RowTile {
     }
     __device__ __forceinline__ int nt(int j) const { return j % (KT / 2) + KT / 2 * half + KT * (j / (KT / 2)); }
 
-    // L R of the page at `base`, L row-major (keys) or transposed with the
-    // values' operand order.
-    template <bool VALUES>
-    __device__ __forceinline__ void product(float (&acc)[8][4], const Layout &y, uint32_t base) const {
+    // += L R, L row-major (keys: at `base`) or transposed (values), R at `R`.
+    template <bool VALUES, bool H16>
+    __device__ __forceinline__ void product(float (&acc)[8][4], const Layout &y, uint32_t base, uint32_t R) const {
         const int rp = VALUES ? y.rvp : y.rkp, pitch = rp * 2, half8 = (lane >> 3) & 1, row8 = (lane & 7) + 8 * (lane >> 4);
-        const uint32_t R = base + (uint32_t)(VALUES ? y.off_RV - y.off_LV : y.off_RK);
         const SwzRows rows16(VALUES ? R : base, VALUES ? row8 : t0 + (lane & 15), pitch);  // the matrix of run-time pitch
         const SwzRows rows8(VALUES ? R : base, VALUES ? lane & 15 : t0 + (lane & 15), pitch);
         int k0 = 0;
@@ -117,8 +182,8 @@ struct RowTile {
                     ldsm_x4(rows16(nt(j), k0 / 8 + half8), b0, b1, b2, b3);
                 else
                     ldsm_x4_t(R + swz_offset(k0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), b0, b1, b2, b3);
-                mma16816(acc[j], a0, a1, a2, a3, b0, b1);
-                mma16816(acc[j + 1], a0, a1, a2, a3, b2, b3);
+                Ops<H16>::mma(acc[j], a0, a1, a2, a3, b0, b1);
+                Ops<H16>::mma(acc[j + 1], a0, a1, a2, a3, b2, b3);
             }
         }
         if (k0 < rp) {  // eight ranks left
@@ -134,8 +199,8 @@ struct RowTile {
                     ldsm_x2(rows8(nt(j), k0 / 8), b0, b1);
                 else
                     ldsm_x2_t(R + swz_offset(k0 + (lane & 7), 16 * nt(j) + 16 * half8, D * 2), b0, b1);
-                mma1688(acc[j], a0, a1, b0);
-                mma1688(acc[j + 1], a0, a1, b1);
+                Ops<H16>::mma8(acc[j], a0, a1, b0);
+                Ops<H16>::mma8(acc[j + 1], a0, a1, b1);
             }
         }
     }
@@ -147,6 +212,35 @@ struct RowTile {
             ldsm_x4(base + swz_offset(t0 + (lane & 15), 16 * nt(j) + 16 * (lane >> 4), D * 2), r0, r1, r2, r3);
             put_pairs(r0, r1, acc[j]);
             put_pairs(r2, r3, acc[j + 1]);
+        }
+    }
+    // The tile's rows of the block whose pages lie at `pages` (INT4 codes and scales at `fetched`).
+    template <bool Q4>
+    __device__ __forceinline__ void rebuild(float (&acc)[8][4], const Layout &y, const BlockLayout &bl, const BlockPages &bp, int kv,
+                                            const unsigned char *pages, const unsigned char *fetched) const {
+#pragma unroll
+        for (int j = 0; j < KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+        const uint32_t base = smem_u32(pages + s * bl.page_bytes);
+        if (s < bp.lo || s >= bp.hi) {
+            rows(acc, base);
+            return;
+        }
+        if (kv) {
+            product<true, Q4>(acc, y, base, base + bl.vR);
+        } else {
+            product<false, Q4>(acc, y, base, base + bl.kR);
+            if (Q4) product<false, Q4>(acc, y, base + (uint32_t)(y.P * y.rkp * 2), base + bl.kR);
+        }
+        if (Q4) {
+            const int g = lane >> 2, c = lane & 3;
+            float row[2] = {1.f, 1.f};
+            if (kv)
+                for (int r2 = 0; r2 < 2; ++r2) row[r2] = bp.token_scale(y, bl, fetched, s, t0 + g + 8 * r2);
+#pragma unroll
+            for (int j = 0; j < KT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[j][e] *= row[e >> 1] * bp.dim_scale(y, bl, fetched, s, kv, 8 * nt(j) + 2 * c + (e & 1));
         }
     }
     // Turn keys stored before RoPE by their positions pg P + t0 + row (the page

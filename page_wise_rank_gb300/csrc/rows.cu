@@ -149,7 +149,7 @@ struct ReadItem {
     }
 };
 
-template <int P, int D>
+template <int P, int D, bool Q4>
 __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
     __shared__ uint64_t bars[2];
@@ -158,18 +158,18 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
     const Layout &y = p.y;
     const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int items = 2 * p.page_off[p.nseq] * y.H;  // page_off: blocks here
-    const uint32_t page_bytes = stage_page_bytes(y);
+    const BlockLayout bl(y);
     if (tid == 0) {
         mbar_init(&bars[0], 1);
         mbar_init(&bars[1], 1);
         fence_barrier_init();
     }
     __syncthreads();
-    auto buffer = [&](int buf) { return sm + TILE + buf * NP * page_bytes; };
+    auto buffer = [&](int buf) { return sm + TILE + buf * NP * bl.fetch_bytes; };
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
         const ReadItem it = its[buf] = ReadItem(p, item, NP);
         BlockPages(y, NP, it.pg0, it.fw, it.kv)
-            .fetch(y, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), page_bytes, &bars[buf]);
+            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf]);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     __syncthreads();
@@ -182,11 +182,11 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
         const ReadItem it = its[buf];
         const int lo = it.lo, hi = it.hi;
         const BlockPages bp(y, NP, it.pg0, it.fw, it.kv);
-        unsigned char *pages = buffer(buf);
+        unsigned char *pages = Q4 ? buffer(2) : buffer(buf);
         if (bp.lo > 0 || bp.hi < NP) {
             // rows past the asked ones are not read: pages of this block past
             // `hi` may be factorized and have no dense rows
-            fetch_dense<P, D>(y, bp, p.dense_pool, nullptr, 0, p.layer, it.b, it.h, it.kv, hi, hi, pages, page_bytes);
+            fetch_dense<P, D>(y, bp, p.dense_pool, nullptr, 0, p.layer, it.b, it.h, it.kv, hi, hi, pages, bl.page_bytes);
             __syncthreads();
         }
         if (bp.lo < bp.hi) {
@@ -203,17 +203,13 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
                 break;
             }
             phase ^= 1u << buf;
+            if (Q4) {
+                bp.expand(y, bl, it.kv, buffer(buf), pages);
+                __syncthreads();
+            }
         }
         float acc[8][4];
-#pragma unroll
-        for (int j = 0; j < rt.KT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-        const uint32_t base = smem_u32(pages + rt.s * page_bytes);
-        if (rt.s < bp.lo || rt.s >= bp.hi)
-            rt.rows(acc, base);
-        else if (it.kv)
-            rt.template product<true>(acc, y, base);
-        else
-            rt.template product<false>(acc, y, base);
+        rt.template rebuild<Q4>(acc, y, bl, bp, it.kv, pages, buffer(buf));
         if (y.rope && it.kv == 0) rt.turn(acc, p.rope_base, p.rope_delta, it.pg0 + rt.s, hi);
 #pragma unroll
         for (int j = 0; j < rt.KT; ++j)
@@ -311,19 +307,19 @@ __global__ void load_factors_kernel(const LoadFactorsParams p) {
     }
 }
 
-template <int P, int D>
+template <int P, int D, bool Q4>
 static cudaError_t read_t(const RowsParams &p, int num_sms, cudaStream_t st) {
-    const int smem = BLOCK * D * 2 + 2 * BLOCK / P * (int)stage_page_bytes(p.y);
-    cudaError_t e = allow_smem<read_kernel<P, D>>(smem);
+    const int smem = BLOCK * D * 2 + (int)BlockLayout(p.y).smem(p.y, BLOCK / P);
+    cudaError_t e = allow_smem<read_kernel<P, D, Q4>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.page_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    read_kernel<P, D><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
+    read_kernel<P, D, Q4><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st) {
     const Layout &y = p.y;
-    if (y.dtype != 1 || y.q4) return launch_rows(p, st);
+    if (y.dtype != 1) return launch_rows(p, st);
     const int np = BLOCK / y.P;
     p.page_off[0] = 0;
     for (int i = 0; i < p.nseq; ++i) {
@@ -331,14 +327,16 @@ cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st) {
         p.page_off[i + 1] = p.page_off[i] + (pages + np - 1) / np;
     }
     if (p.page_off[p.nseq] == 0) return cudaSuccess;
-    if (y.d == 64) {
-        if (y.P == 16) return read_t<16, 64>(p, num_sms, st);
-        if (y.P == 32) return read_t<32, 64>(p, num_sms, st);
-        return read_t<64, 64>(p, num_sms, st);
-    }
-    if (y.P == 16) return read_t<16, 128>(p, num_sms, st);
-    if (y.P == 32) return read_t<32, 128>(p, num_sms, st);
-    return read_t<64, 128>(p, num_sms, st);
+#define PKV_READ_CASE(PP, DD) \
+    if (y.P == PP && y.d == DD) return y.q4 ? read_t<PP, DD, true>(p, num_sms, st) : read_t<PP, DD, false>(p, num_sms, st);
+    PKV_READ_CASE(16, 64)
+    PKV_READ_CASE(32, 64)
+    PKV_READ_CASE(64, 64)
+    PKV_READ_CASE(16, 128)
+    PKV_READ_CASE(32, 128)
+    PKV_READ_CASE(64, 128)
+#undef PKV_READ_CASE
+    return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st) {
