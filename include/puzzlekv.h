@@ -390,10 +390,12 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t la
  *            max_tokens_per_seq with the cached ones.
  *   work:    device, 256-byte aligned, work_bytes >= what
  *            puzzlekv_chunk_workspace reports; its contents are scratch.
- * The call may be captured into a CUDA graph once puzzlekv_wait_background has
- * been called on the capturing stream; a replay attends the store's content at
- * the lengths it was captured with.  Graphs that may run at the same time need
- * workspaces of their own.
+ * The call may be captured into a CUDA graph when no background work of the
+ * store is pending (puzzlekv_wait_background before the capture;
+ * PUZZLEKV_ERR_UNSUPPORTED otherwise); a replay attends the store's content at
+ * the lengths it was captured with.  Calls that may run at the same time, on
+ * two streams or in two graphs, need workspaces of their own.  If a bounded wait
+ * runs out (puzzlekv_check_device_status), the call's outputs are undefined.
  */
 puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *store, int32_t layer, const void *q, const void *k,
                                          const void *v, void *out, const int32_t *seq_ids, const int32_t *counts,

@@ -358,6 +358,8 @@ class Store:
             if N == 0:
                 return out
             work = workspace if workspace is not None else self._scratch(nb.value)
+            if work.device != self.dense_pool.device or not work.is_contiguous():
+                raise ValueError("workspace must be a contiguous tensor on the store's device")
             check(lib().puzzlekv_chunk_attention(self._h, layer, _ptr(q), _ptr(k), _ptr(v), _ptr(out), ids, cnt, B,
                                                  _ptr(work), work.numel() * work.element_size(), self._queue(stream)))
         return out

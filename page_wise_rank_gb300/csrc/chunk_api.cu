@@ -45,6 +45,19 @@ puzzlekv_status refuse_capture(cudaStream_t strm) {
     return PUZZLEKV_OK;
 }
 
+// A captured call cannot wait for background work queued outside the capture.
+puzzlekv_status refuse_pending(const puzzlekv_store *s, cudaStream_t strm) {
+    bool pending = false;
+    for (const auto &cb : s->batches) pending |= cb.pending;
+    if (!pending) return PUZZLEKV_OK;
+    cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing(strm, &c);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+    if (c != cudaStreamCaptureStatusNone)
+        return fail(PUZZLEKV_ERR_UNSUPPORTED, "background conversions are pending: call puzzlekv_wait_background before the capture");
+    return PUZZLEKV_OK;
+}
+
 puzzlekv_status check_list(const puzzlekv_store *s, const int32_t *ids, int32_t B, const char *what) {
     if (!s) return fail(PUZZLEKV_ERR_INVALID_ARG, "store is NULL");
     if (B < 1 || B > MAX_CALL_BATCH) return fail(PUZZLEKV_ERR_INVALID_ARG, "B must be in [1, %d]", MAX_CALL_BATCH);
@@ -169,7 +182,7 @@ void split_flash(const puzzlekv_store *s, FlashParams &f) {
         const std::vector<long long> &u = before[eh / f.H];
         const long long r = u0 - head_off[eh];
         const int pair = (int)(std::upper_bound(u.begin(), u.end(), r) - u.begin()) - 1;
-        f.share[c] = {eh / f.H, eh % f.H, pair, (int)(r - u[pair]), (int)(u1 - u0)};
+        f.share[c] = {eh / f.H, eh % f.H, pair, (int)(r - u[pair]), u1 - u0};
     }
 }
 
@@ -348,6 +361,8 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
         st = check_work(work, work_bytes, pl.bytes);
         if (st != PUZZLEKV_OK) return st;
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        st = refuse_pending(s, strm);
+        if (st != PUZZLEKV_OK) return st;
         char *w = static_cast<char *>(work);
         wait_conversions(s, strm, pl.seqs, pl.lens, pl.nseq);
         s->after_decode = false;
@@ -564,6 +579,8 @@ puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int
         rp.row_stride = (size_t)y.H * y.d;
         rp.head_stride = y.d;
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
+        st = refuse_pending(s, strm);
+        if (st != PUZZLEKV_OK) return st;
         wait_conversions(s, strm, seq_ids, lens, B);
         s->after_decode = false;
         const cudaError_t e = launch_read(rp, s->num_sms, strm);

@@ -23,7 +23,8 @@ constexpr int RING = 5;  // key / value images in flight: what is left of shared
 // The pieces of one CTA's share of the units, in order.
 struct Pieces {
     const FlashParams &p;
-    int left, i, h, pair, b0;
+    long long left;
+    int i, h, pair, b0;
     // the current piece: blocks [cb0, cb1) of cnb; the share's first piece?
     int ci, ch, cpair, cb0, cb1, cnb;
     bool cfirst;
@@ -37,7 +38,7 @@ struct Pieces {
         cfirst = cnb == 0;
         ci = i; ch = h; cpair = pair; cb0 = b0;
         cnb = flash_blocks(p.T[i], p.n[i], p.G, pair);
-        cb1 = min(cnb, b0 + left);
+        cb1 = (int)min((long long)cnb, b0 + left);
         left -= cb1 - cb0;
         b0 = 0;
         if ((pair + 1) * FLASH_ROWS < p.n[i] * p.G) {
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
     const int nb = flash_blocks(p.T[i], p.n[i], p.G, pr);
     const int c0 = blockIdx.x;  // the CTA that begins the pair
     int c1 = c0 + 1;            // and the one that ends it
-    for (int at = cut.b0 + cut.units; at < nb; at += p.share[c1].units) ++c1;
+    for (long long at = cut.b0 + cut.units; at < nb; at += p.share[c1].units) ++c1;
     const int np = c1 - c0 + 1, slot0 = before.units == cut.b0 ? 2 * c0 : 2 * c0 + 1;
     const int R = p.n[i] * p.G;
     constexpr int V = D / 32;

@@ -232,7 +232,8 @@ struct FlashParams {
     long long units;  // of all entries
     // share of CTA c: units[c] units from block b0 of (entry, head, pair) on
     struct Share {
-        int i, h, pair, b0, units;
+        int i, h, pair, b0;
+        long long units;
     } share[FLASH_MAX_CTAS];
 };
 

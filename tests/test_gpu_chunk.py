@@ -188,6 +188,11 @@ def test_workspace_given_and_too_small(pkv):
     assert torch.equal(out, store.chunk_attention(0, q, k, v, [0], [9], workspace=work))
     with pytest.raises(pkv.PuzzleKVError, match="workspace"):
         store.chunk_attention(0, q, k, v, [0], [9], workspace=work[:need["attention"] - 256])
+    with pytest.raises(pkv.PuzzleKVError, match="workspace"):
+        store.chunk_attention(0, q, k, v, [0], [9], workspace=torch.empty(need["attention"] + 64, dtype=torch.uint8,
+                                                                         device="cuda")[64:])
+    with pytest.raises(ValueError, match="workspace"):
+        store.chunk_attention(0, q, k, v, [0], [9], workspace=work.cpu())
 
 
 def test_capture_and_replay(pkv):
@@ -247,6 +252,120 @@ def test_side_stream(pkv):
     kc, vc = kr[-100:].clone(), vr[-100:].clone()  # the window's rows are exact
     assert torch.equal(kc, k[-100:]) and torch.equal(vc, v[-100:])
     assert check_attention(store, cfg, host, 0, [0], [700], [150], q.cpu(), k.cpu(), v.cpu(), out) <= 1.0
+
+
+def test_values_of_every_size(pkv):
+    """Value and key magnitudes from 1e-9 to 1e9, page by page and inside the chunk: the operand images' scales."""
+    cfg = make_cfg(pkv, num_layers=1, max_batch=1)
+    T = 1000
+    for n in (6, 150):
+        g = torch.Generator().manual_seed(n)
+        K, V = random_rows(cfg, T, 70, 1)
+        page = torch.arange(T) // 64
+        V = (V.float() * (10.0 ** torch.randint(-9, 10, (17,), generator=g).float())[page][None, None, :, None]).to(cfg.kv_dtype)
+        K = (K.float() * (10.0 ** torch.randint(-9, 1, (17,), generator=g).float())[page][None, None, :, None]).to(cfg.kv_dtype)
+        store, host = pkv.Store(cfg), HostCache()
+        store.load_prefill(0, K.cuda(), V.cuda())
+        host.set_prefill(0, K, V)
+        k, v = random_rows(cfg, n, 71)
+        v = (v.float() * (10.0 ** torch.randint(-6, 7, (n, 1, 1), generator=g).float())).to(cfg.kv_dtype)
+        q = queries(cfg, n, 72)
+        out = store.chunk_attention(0, q.cuda(), k.cuda(), v.cuda(), [0], [n])
+        assert check_attention(store, cfg, host, 0, [0], [T], [n], q, k, v, out) <= 1.0
+
+
+@pytest.mark.parametrize("kw", [dict(rank_k=48, rank_v=24), dict(rank_k=1, rank_v=64), dict(rank_k=64, rank_v=8),
+                                dict(num_kv_heads=1, num_q_heads=7), dict(recent_tokens=1000), dict(sink_tokens=300)])
+def test_wide_ranks_heads_and_windows(pkv, kw):
+    cfg = make_cfg(pkv, num_layers=1, **kw)
+    lens, counts = [1500, 1, 640, 129], [5, 17, 1, 90]
+    store, host = filled(pkv, cfg, lens)
+    k, v = random_rows(cfg, sum(counts), 31)
+    q = queries(cfg, sum(counts), 32)
+    out = store.chunk_attention(0, q.cuda(), k.cuda(), v.cuda(), [0, 1, 2, 3], counts)
+    assert check_attention(store, cfg, host, 0, [0, 1, 2, 3], lens, counts, q, k, v, out) <= 1.0
+    kr, vr = store.read_tokens(0, [0], [0], [1500])
+    K, V, Ka, Va = cache_rows(store, cfg, host, 0, 0, 1500)
+    for got, X, Xa in ((kr, K, Ka), (vr, V, Va)):
+        bound = U[cfg.kv_dtype] * np.abs(X) + 84 * U32 * Xa
+        assert excess(got, X.transpose(1, 0, 2), bound.transpose(1, 0, 2) * 1.01) <= 1.0
+
+
+@pytest.mark.parametrize("name", ["llama", "g1-p16", "int4", "fp32"])
+def test_sixty_four_sequences(pkv, name):
+    """The longest list, lengths from empty to several pages, one to a few tokens and two longer chunks."""
+    cfg = make_cfg(pkv, num_layers=1, max_batch=64, max_tokens_per_seq=700, **STORES[name])
+    rng = np.random.RandomState(2)
+    lens = [int(x) for x in rng.randint(0, 500, 64)]
+    counts = [int(x) for x in rng.randint(0, 7, 64)]
+    counts[5], counts[40] = 130, 77
+    ids = [int(x) for x in rng.permutation(64)]
+    store, host = filled(pkv, cfg, lens)
+    N = sum(counts)
+    k, v = random_rows(cfg, N, 41)
+    q = queries(cfg, N, 42)
+    out = store.chunk_attention(0, q.cuda(), k.cuda(), v.cuda(), ids, counts)
+    assert check_attention(store, cfg, host, 0, ids, [lens[b] for b in ids], counts, q, k, v, out) <= 1.0
+    store.append_chunk(0, k.cuda(), v.cuda(), ids, counts)
+    for b, n in zip(ids, counts):
+        if lens[b] + n:
+            check_page_table(store, cfg, b, 0, lens[b] + n)
+    assert store.check_device_status() == 0
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_long_context(pkv, n):
+    cfg = make_cfg(pkv, num_layers=1, num_kv_heads=1, num_q_heads=4, max_batch=1, max_tokens_per_seq=70000)
+    T = 65537
+    store, host = filled(pkv, cfg, [T])
+    k, v = random_rows(cfg, n, 1)
+    q = queries(cfg, n, 2)
+    out = store.chunk_attention(0, q.cuda(), k.cuda(), v.cuda(), [0], [n])
+    assert check_attention(store, cfg, host, 0, [0], [T], [n], q, k, v, out) <= 1.0
+
+
+def test_two_streams_at_once(pkv):
+    cfg = make_cfg(pkv)
+    store, _ = filled(pkv, cfg, [900, 500, 0, 0])
+    jobs = []
+    for i, (ids, counts) in enumerate([([0], [4]), ([1], [200]), ([0, 1], [120, 3]), ([0], [90])]):
+        N = sum(counts)
+        k, v = (x.cuda() for x in random_rows(cfg, N, i))
+        q = queries(cfg, N, i).cuda()
+        jobs.append((ids, counts, q, k, v, store.chunk_attention(0, q, k, v, ids, counts)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for _ in range(5):
+        got = [store.chunk_attention(0, q, k, v, ids, counts, stream=s)
+               for s, (ids, counts, q, k, v, _) in zip(streams, jobs)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b[-1]) for a, b in zip(got, jobs))
+
+
+def test_pending_conversions_refuse_a_capture(pkv):
+    cfg = make_cfg(pkv)
+    store, _ = filled(pkv, cfg, [640, 0, 0, 0])
+    k, v = (x.cuda() for x in random_rows(cfg, 3, 1))
+    q = queries(cfg, 3, 2).cuda()
+    want = store.chunk_attention(0, q, k, v, [0], [3])
+    out = torch.zeros_like(q)
+    store.convert_ready_pages()  # a batch on the internal stream
+    g = torch.cuda.CUDAGraph()
+    refused = False
+    with torch.cuda.graph(g):
+        torch.zeros(1, device="cuda")
+        try:
+            store.chunk_attention(0, q, k, v, [0], [3], out=out)
+        except pkv.PuzzleKVError as e:
+            refused = "pending" in str(e)
+    assert refused
+    store.wait_background()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        store.chunk_attention(0, q, k, v, [0], [3], out=out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 # ---------------------------------------------------------------- rows
