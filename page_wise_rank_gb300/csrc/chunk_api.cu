@@ -161,29 +161,49 @@ void split_small(const puzzlekv_store *s, SmallParams &p) {
     }
 }
 
-// The shares of the tensor-memory path's CTAs.
+// The shares of the tensor-memory path's CTAs.  A piece costs its blocks and
+// about kPiece more (queries in, output out, an empty pipeline at both ends), so
+// the shares are cut where the costs come out even: without that, a CTA of many
+// short pieces (first chunks of prompts) took three times as long as one of
+// long pieces.
 void split_flash(const puzzlekv_store *s, FlashParams &f) {
-    // units before each pair of every entry, one head
-    std::vector<std::vector<long long>> before(f.nseq);
-    std::vector<long long> head_off;  // units before (entry, head), in order
-    long long U = 0;
+    constexpr int kPiece = 4;
+    // costs and blocks before each pair of every entry, one head
+    struct Before {
+        long long cost, blocks;
+    };
+    std::vector<std::vector<Before>> pairs(f.nseq);
+    std::vector<Before> heads;  // before (entry, head), in order
+    Before all{0, 0};
     for (int j = 0; j < f.nseq; ++j) {
-        std::vector<long long> &u = before[j];
-        u.push_back(0);
-        for (int p = 0; (long long)p * FLASH_ROWS < (long long)f.n[j] * f.G; ++p)
-            u.push_back(u.back() + flash_blocks(f.T[j], f.n[j], f.G, p));
-        for (int h = 0; h < f.H; ++h, U += u.back()) head_off.push_back(U);
+        Before u{0, 0};
+        for (int p = 0; (long long)p * FLASH_ROWS < (long long)f.n[j] * f.G; ++p) {
+            pairs[j].push_back(u);
+            const int nb = flash_blocks(f.T[j], f.n[j], f.G, p);
+            u.cost += nb + kPiece;
+            u.blocks += nb;
+        }
+        for (int h = 0; h < f.H; ++h, all.cost += u.cost, all.blocks += u.blocks) heads.push_back(all);
     }
-    f.units = U;
-    f.ctas = (int)std::min<long long>(std::min(s->num_sms, FLASH_MAX_CTAS), U);
-    for (int c = 0; c < f.ctas; ++c) {
-        const long long u0 = U * c / f.ctas, u1 = U * (c + 1) / f.ctas;
-        const int eh = (int)(std::upper_bound(head_off.begin(), head_off.end(), u0) - head_off.begin()) - 1;
-        const std::vector<long long> &u = before[eh / f.H];
-        const long long r = u0 - head_off[eh];
-        const int pair = (int)(std::upper_bound(u.begin(), u.end(), r) - u.begin()) - 1;
-        f.share[c] = {eh / f.H, eh % f.H, pair, (int)(r - u[pair]), u1 - u0};
+    f.units = all.blocks;
+    const int most = (int)std::min<long long>(std::min(s->num_sms, FLASH_MAX_CTAS), all.blocks);
+    auto below = [](long long x, const Before &e) { return x < e.cost; };
+    f.ctas = 0;
+    long long last = -1;
+    for (int c = 0; c < most; ++c) {
+        const long long x = all.cost * c / most;
+        const int eh = (int)(std::upper_bound(heads.begin(), heads.end(), x, below) - heads.begin()) - 1;
+        const std::vector<Before> &u = pairs[eh / f.H];
+        const long long r = x - heads[eh].cost;
+        const int pair = (int)(std::upper_bound(u.begin(), u.end(), r, below) - u.begin()) - 1;
+        const int b0 = (int)std::max<long long>(0, r - u[pair].cost - kPiece);
+        const long long at = heads[eh].blocks + u[pair].blocks + b0;
+        if (at == last) continue;  // no empty shares
+        if (f.ctas) f.share[f.ctas - 1].units = at - last;
+        f.share[f.ctas++] = {eh / f.H, eh % f.H, pair, b0, 0};
+        last = at;
     }
+    f.share[f.ctas - 1].units = all.blocks - last;
 }
 
 void plan_attention(const puzzlekv_store *s, int32_t layer, const int32_t *seq_ids, const int32_t *counts, int32_t B,
