@@ -533,8 +533,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 uint32_t o[32];
                 tmem_ld32(tO + 32 * k, o);
                 tc_wait_ld();
-                if (!live) continue;
-                if (whole) {
+                if (live && whole) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 8) {
                         auto pk = [&](int a) {
@@ -542,13 +541,14 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                         };
                         *reinterpret_cast<uint4 *>(out + (32 * k + e) * 2) = make_uint4(pk(0), pk(2), pk(4), pk(6));
                     }
-                } else {
+                } else if (live) {
 #pragma unroll
                     for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<float4 *>(part + 4 + 32 * k + e) =
                             make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
                                         __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
                 }
+                __syncwarp();  // the next read is the whole warp's
             }
         }
     } else {
