@@ -57,8 +57,21 @@ __device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4], float sc
         for (int t = 0; t < NT; ++t) mx = fmaxf(mx, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(w.m[r], mx * scale), base = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2s(w.m[r] - base);
+        // The reference moves only when a score exceeds it by 2^8: the weights
+        // are split to 16 bits whatever their size, and o is rescaled rarely.
+        const float top = mx * scale;
+        const bool move = top > w.m[r] + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+            const float f = move ? ex2s(w.m[r] - top) : 1.f;
+            if (move) w.m[r] = top;
+            w.l[r] *= f;
+#pragma unroll
+            for (int t = 0; t < D / 8; ++t) {
+                w.o[t][2 * r] *= f;
+                w.o[t][2 * r + 1] *= f;
+            }
+        }
+        const float base = w.m[r] == -INFINITY ? 0.f : w.m[r];
         float ls = 0.f;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -67,14 +80,7 @@ __device__ __forceinline__ void fold(RowState<D> &w, float (&s)[NT][4], float sc
                 s[t][2 * r + e] = ex2s(fmaf(s[t][2 * r + e], scale, -base));
                 ls += s[t][2 * r + e];
             }
-        w.l[r] = fmaf(w.l[r], f, ls);  // this lane's columns; the quad's sums join at the end
-        w.m[r] = mn;
-        if (__any_sync(0xffffffffu, f != 1.f))
-#pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-                w.o[t][2 * r] *= f;
-                w.o[t][2 * r + 1] *= f;
-            }
+        w.l[r] += ls;  // this lane's columns; the quad's sums join at the end
     }
 }
 
@@ -113,13 +119,18 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
         int k0 = 0;
 #pragma unroll 1
         for (; k0 + 16 <= y.rkp; k0 += 16) {
-            float t[4][4] = {};  // even and odd steps apart: shorter chains
+            float t[4][4];  // even and odd steps apart: shorter chains
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 uint32_t b0, b1, b2, b3;
                 ldsm_x4(RK + swz_offset(k0 + row8, 32 * ks + 16 * half, D * 2), b0, b1, b2, b3);
-                mma16816(t[2 * (ks & 1)], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
-                mma16816(t[2 * (ks & 1) + 1], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b2, b3);
+                if (ks < 2) {
+                    mma16816_first(t[2 * ks], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
+                    mma16816_first(t[2 * ks + 1], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b2, b3);
+                } else {
+                    mma16816(t[2 * (ks & 1)], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b0, b1);
+                    mma16816(t[2 * (ks & 1) + 1], w.q[ks][0], w.q[ks][1], w.q[ks][2], w.q[ks][3], b2, b3);
+                }
             }
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -165,11 +176,18 @@ __device__ __forceinline__ void page_unit(RowState<D> &w, const Layout &y, uint3
     int k0 = 0;
 #pragma unroll 1
     for (; k0 + 16 <= y.rvp; k0 += 16) {
-        float u[4][4] = {};  // weights' high parts and residuals apart
+        float u[4][4];  // weights' high parts and residuals apart
 #pragma unroll
         for (int k = 0; k < P / 16; ++k) {
             uint32_t b0, b1, b2, b3;
             ldsm_x4(LV + swz_offset(k0 + row8, 32 * k + 16 * half, P * 2), b0, b1, b2, b3);
+            if (k == 0) {
+                mma16816_first(u[0], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b0, b1);
+                mma16816_first(u[1], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b2, b3);
+                mma16816_first(u[2], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b0, b1);
+                mma16816_first(u[3], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b2, b3);
+                continue;
+            }
             mma16816(u[0], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b0, b1);
             mma16816(u[1], ph[k][0], ph[k][1], ph[k][2], ph[k][3], b2, b3);
             mma16816(u[2], pl[k][0], pl[k][1], pl[k][2], pl[k][3], b0, b1);
