@@ -120,10 +120,12 @@ void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
 }
 
 // Splits of the few-token path's entries over the SMs (one CTA each): every KV
-// head's CTAs go to the entries in proportion to the bytes they stream.  One
-// wave of CTAs is best when the shares come out even; lists of unequal lengths
-// fill the SMs better with up to four.  A CTA's start and merge cost about as
-// much as streaming 110 KB.
+// head's CTAs go to the entries in proportion to what they cost, the bytes they
+// stream, times 1.6, 3.2 or 6.4 where two, four or eight row tiles make the
+// arithmetic of a page (about 1,050 cycles a row-tile pair) longer than its
+// 670 cycles of memory time.  One wave of CTAs is best when the shares come out even;
+// lists of unequal lengths fill the SMs better with up to four.  A CTA's start
+// and merge cost about as much as streaming 110 KB.
 void split_small(const puzzlekv_store *s, SmallParams &p) {
     const Layout &y = s->y;
     constexpr double kCta = 110e3;
@@ -132,7 +134,8 @@ void split_small(const puzzlekv_store *s, SmallParams &p) {
     double total = 0, best = 0;
     for (int i = 0; i < p.nseq; ++i) {
         const PageSplit ps(p.T[i], y.P, y.sink_pages, y.sink_tokens, y.W, rec, half, 1);
-        cost[i] = (double)ps.total + (double)p.n[i] * y.d * 2 * y.esz;
+        const int tiles = (p.n[i] * y.G + 15) / 16;
+        cost[i] = ((double)ps.total + (double)p.n[i] * y.d * 2 * y.esz) * (tiles <= 1 ? 1.0 : tiles <= 2 ? 1.6 : tiles <= 4 ? 3.2 : 6.4);
         total += cost[i];
     }
     std::vector<int> ns(p.nseq), pick(p.nseq, 1);
