@@ -364,7 +364,10 @@ puzzlekv_status puzzlekv_decode_attention_static_scratch(puzzlekv_store *store, 
 /*
  * Workspace bytes of puzzlekv_chunk_attention and puzzlekv_append_chunk for
  * these arguments at the sequences' present lengths (either pointer may be
- * NULL).  Host-only.
+ * NULL).  Attention of more than 128 query rows per KV head (of any number in
+ * stores with INT4 records, keys before RoPE or fp32) lays the sequence out
+ * densely: 2 (T + count) num_kv_heads head_dim elements of kv_dtype, to 128
+ * tokens; fewer need only split states, a few MB.  Host-only.
  */
 puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t layer, const int32_t *seq_ids,
                                          const int32_t *counts, int32_t B, size_t *attention_bytes,

@@ -376,7 +376,9 @@ class Store:
         self._need_here(v, (N, c.num_kv_heads, c.head_dim), "v")
         with self._on(stream):
             nb = ctypes.c_size_t()
-            check(lib().puzzlekv_chunk_workspace(self._h, layer, ids, cnt, B, None, ctypes.byref(nb)))
+            # a chunk of at most a page never outgrows the ring
+            if max(cnt[:B], default=0) > c.page_size or N == 0:
+                check(lib().puzzlekv_chunk_workspace(self._h, layer, ids, cnt, B, None, ctypes.byref(nb)))
             if N == 0:
                 return
             work = self._scratch(nb.value) if nb.value else None

@@ -1,5 +1,5 @@
-// Attention of a chunk of query tokens over densely laid out keys and values
-// in CUDA-core fp32 arithmetic, and the merge of split softmax states
+// Attention of a chunk of query tokens over densely laid out fp32 keys and
+// values in CUDA-core arithmetic (fp32 stores), and the merge of split softmax states
 // ("PuzzleKV: Page-Wise Low-Rank Decomposition for KV Cache Compression",
 // §3.3 ④, eq. (5)).
 //
@@ -17,15 +17,13 @@ namespace pkv {
 constexpr int CS_ROWS = 32, CS_KEYS = 32;  // query rows and keys of a tile
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 v = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(bf16_lo_to_f32(v.x), bf16_hi_to_f32(v.x), bf16_lo_to_f32(v.y), bf16_hi_to_f32(v.y));
-}
 
 // Block (tile of 32 query rows of one (entry, KV head), split): 128 threads,
 // eight to a pair of rows.  A thread scores 2 rows x 4 keys and accumulates
-// 2 rows x D/8 columns, so that a shared-memory vector feeds two rows.
-template <typename T, int D>
+// 2 rows x D/8 columns, so that a shared-memory vector feeds two rows.  Bound by
+// shared-memory reads where there is much work, by its few dependent tiles where
+// there is little (37 tokens over 1K, d = 64: 13 us).
+template <int D>
 __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams p) {
     extern __shared__ __align__(16) float sm[];
     constexpr int PQ = D + 4;  // row pitch: the four row groups of a warp start on distinct banks
@@ -40,7 +38,7 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
     const int h = u / tiles, row0 = (u % tiles) * CS_ROWS;
     const int Tk = p.T[i] + p.n[i], nkb = (Tk + CS_KEYS - 1) / CS_KEYS;
     const int kb0 = (int)((long long)nkb * sp / ns), kb1 = (int)((long long)nkb * (sp + 1) / ns);
-    const T *q = reinterpret_cast<const T *>(p.q);
+    const float *q = reinterpret_cast<const float *>(p.q);
     constexpr int PER = CS_KEYS * D / 4 / 128;  // groups of four elements of a tile per thread
     {
         float4 v[PER];
@@ -67,8 +65,8 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
         for (int c = 0; c < D / 8; ++c) o[a][c] = 0.f;
     }
     const int last_key = p.T[i] + (min(row0 + CS_ROWS, R) - 1) / G;
-    const T *K = reinterpret_cast<const T *>(p.K) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
-    const T *V = reinterpret_cast<const T *>(p.V) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
+    const float *K = reinterpret_cast<const float *>(p.K) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
+    const float *V = reinterpret_cast<const float *>(p.V) + (size_t)p.koff[i] * p.H * D + (size_t)h * D;
     for (int kb = kb0; kb < kb1 && kb * CS_KEYS <= last_key; ++kb) {
         float4 kr[PER], vr[PER];  // in flight together, past the last tile's arithmetic
 #pragma unroll
@@ -150,9 +148,11 @@ __global__ void __launch_bounds__(128) chunk_simple_kernel(const ChunkAttnParams
         if (r >= R) continue;
         if (ns == 1) {
             const float il = 1.f / l[a];
-            T *dst = reinterpret_cast<T *>(p.out) + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D;
+            float *dst = reinterpret_cast<float *>(p.out) + ((size_t)(p.off[i] + r / G) * p.Hq + h * G + r % G) * D;
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) dst[32 * (c / 4) + 4 * tx + c % 4] = Elem<T>::from_f32(o[a][c] * il);
+            for (int c4 = 0; c4 < D / 32; ++c4)
+                *reinterpret_cast<float4 *>(dst + 32 * c4 + 4 * tx) =
+                    make_float4(o[a][4 * c4] * il, o[a][4 * c4 + 1] * il, o[a][4 * c4 + 2] * il, o[a][4 * c4 + 3] * il);
         } else {
             float *row = p.partials + (size_t)(p.poff[i] + (long long)(h * ns + sp) * R + r) * (D + 4);
             if (tx == 0) *reinterpret_cast<float4 *>(row) = make_float4(m[a], l[a], 0.f, 0.f);
@@ -214,22 +214,21 @@ __global__ void __launch_bounds__(128) chunk_merge_kernel(const ChunkAttnParams 
     for (int k = 0; k < V; ++k) dst[lane * V + k] = Elem<T>::from_f32(acc[k] * il);
 }
 
-template <typename T, int D>
+template <int D>
 static cudaError_t simple_t(ChunkAttnParams &p, cudaStream_t st) {
     constexpr int smem = ((CS_ROWS + 2 * CS_KEYS) * (D + 4) + CS_ROWS * (CS_KEYS + 1)) * 4;
-    cudaError_t e = allow_smem<chunk_simple_kernel<T, D>>(smem);
+    cudaError_t e = allow_smem<chunk_simple_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
-    chunk_simple_kernel<T, D><<<(unsigned)p.tile_off[p.nseq], 128, smem, st>>>(p);
+    chunk_simple_kernel<D><<<(unsigned)p.tile_off[p.nseq], 128, smem, st>>>(p);
     return cudaGetLastError();
 }
 
-cudaError_t launch_chunk_simple(ChunkAttnParams &p, int dtype, cudaStream_t st) {
+cudaError_t launch_chunk_simple(ChunkAttnParams &p, cudaStream_t st) {
     p.tile_off[0] = 0;
     for (int i = 0; i < p.nseq; ++i)
         p.tile_off[i + 1] = p.tile_off[i] + p.H * ((p.n[i] * p.G + CS_ROWS - 1) / CS_ROWS) * p.ns[i];
     if (p.tile_off[p.nseq] == 0) return cudaSuccess;
-    if (dtype == 1) return p.d == 64 ? simple_t<__nv_bfloat16, 64>(p, st) : simple_t<__nv_bfloat16, 128>(p, st);
-    return p.d == 64 ? simple_t<float, 64>(p, st) : simple_t<float, 128>(p, st);
+    return p.d == 64 ? simple_t<64>(p, st) : simple_t<128>(p, st);
 }
 
 cudaError_t launch_chunk_merge(const ChunkAttnParams &q, int dtype, cudaStream_t st) {

@@ -116,7 +116,6 @@ void rows_params(const puzzlekv_store *s, int layer, RowsParams &rp) {
     rp.rope_base = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_base_offset);
     rp.rope_delta = reinterpret_cast<const float2 *>(s->workspace + s->y.rope_delta_offset);
     rp.layer = layer;
-    rp.turn = 1;
 }
 
 // Splits of the few-token path's entries over the SMs (one CTA each): every KV
@@ -431,7 +430,7 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
             a.K = r.k_out;
             a.V = r.v_out;
             e = launch_rows(r, strm);
-            if (e == cudaSuccess) e = launch_chunk_simple(a, y.dtype, strm);
+            if (e == cudaSuccess) e = launch_chunk_simple(a, strm);
         }
         if (a.nseq && e == cudaSuccess) e = launch_chunk_merge(a, y.dtype, strm);
         if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
@@ -499,7 +498,6 @@ puzzlekv_status puzzlekv_append_chunk(puzzlekv_store *s, int32_t layer, const vo
             const size_t half = gather_bytes(y, lp) / 2;
             RowsParams rp;
             rows_params(s, layer, rp);
-            rp.turn = 0;
             rp.k_new = ap.k;
             rp.v_new = ap.v;
             rp.k_out = static_cast<char *>(work) + at;

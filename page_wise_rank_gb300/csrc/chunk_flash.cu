@@ -141,10 +141,11 @@ __device__ __forceinline__ float finite_abs(float x) {
 // (Rebuilt keys and values in bf16 left 6e-3 of the output's norm at 32K tokens,
 // 3.5 times the output's own rounding.)
 //
-// HBM-bound: 40 % of the image bytes are read, all are written.  Every step of
+// HBM-bound: 47 % of the image bytes are read, all are written.  Every step of
 // an item is short and waits on the one before, so CTAs stay and loop over
 // items: the next item's factors arrive and the last image leaves while one is
-// computed.
+// computed.  32K tokens x 8 heads, ranks 16 and 24: 51 us (3.9 TB/s; 82 us with a
+// CTA per block and 8 warps); INT4 records, whose codes are expanded first: 150 us.
 struct StageItem {
     int i, b, T0, T1, fw, h, blk, kv;
     StageItem() = default;

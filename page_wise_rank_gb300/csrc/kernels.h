@@ -104,7 +104,7 @@ struct AppendParams {
 
 // Rows of the cache of a list of sequences, as attention sees them: row t of
 // call entry i comes from the store for t < T[i] (factorized pages rebuilt as
-// L R, keys stored before RoPE turned when `turn` is set) and from the chunk
+// L R, by launch_read with keys stored before RoPE turned) and from the chunk
 // k_new / v_new ([sum n][H][d], entry i's tokens from row coff[i] on) beyond.
 // Rows lo[i] .. lo[i] + n[i] - 1 go to k_out / v_out: row r of the call's rows
 // (entry i's from off[i] on) at element r * row_stride + head * head_stride.
@@ -116,7 +116,7 @@ struct RowsParams {
     char *k_out, *v_out;
     int *status;
     size_t row_stride, head_stride;  // elements
-    int layer, nseq, turn;
+    int layer, nseq;
     int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], lo[MAX_CALL_BATCH], n[MAX_CALL_BATCH];
     int off[MAX_CALL_BATCH], coff[MAX_CALL_BATCH];
     int fw[MAX_CALL_BATCH];  // launch_read: page after the last factorized one
@@ -273,14 +273,15 @@ cudaError_t launch_small(SmallParams &p, cudaStream_t st);
 cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st);
 
+// fp32 stores: any rows.  bf16 stores: dense and chunk rows, keys as stored.
 cudaError_t launch_rows(RowsParams &p, cudaStream_t st);
-// launch_rows for rows of the cache alone (no chunk rows).
+// Rows of the cache alone (no chunk rows), any store.
 cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st);
 cudaError_t launch_append_chunk(const AppendChunkParams &p, cudaStream_t st);
 cudaError_t launch_truncate(const TruncateParams &p, cudaStream_t st);
 cudaError_t launch_load_factors(const LoadFactorsParams &p, cudaStream_t st);
 cudaError_t launch_copy(CopyParams &p, int num_sms, cudaStream_t st);
-cudaError_t launch_chunk_simple(ChunkAttnParams &p, int dtype, cudaStream_t st);
+cudaError_t launch_chunk_simple(ChunkAttnParams &p, cudaStream_t st);  // fp32
 cudaError_t launch_chunk_merge(const ChunkAttnParams &p, int dtype, cudaStream_t st);
 
 cudaError_t launch_factorize(const FactorParams &p, int num_sms, cudaStream_t st);

@@ -10,61 +10,13 @@
 
 namespace pkv {
 
-// Dequantize one factor of an INT4 record (K x N operand starting at register
-// m0 of the stream) to fp32 at put(k, n, code).
-template <typename F>
-__device__ __forceinline__ void q4_codes(const char *stream, int m0, int K, int N, F put) {
-    const int regs = q4_operand_regs(K, N);
-    for (int i = threadIdx.x; i < regs * 32; i += blockDim.x) {
-        const int m = m0 + i / 32, lane = i % 32, w = m / 4;
-        const uint32_t word = *reinterpret_cast<const uint32_t *>(stream + ((w / 2) * 32 + lane) * 8 + (w % 2) * 4);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            int k, n;
-            q4_operand_elem(K, N, m - m0, lane, e, k, n);
-            put(k, n, (float)((int)((word >> (4 * ((m % 4) + 4 * e))) & 15u) - 8));
-        }
-    }
-}
-
-// A page's factors in fp32: L [P][rp] at `Ls`, R [rp][d] at `Rs` (shared memory).
-template <typename T>
-__device__ void load_page_factors(const Layout &y, const char *rec, int kv, float *Ls, float *Rs) {
-    const int P = y.P, d = y.d, rp = kv == 0 ? y.rkp : y.rvp;
-    if (y.q4) {
-        auto sc = [&](size_t off, int i) {
-            return __half2float(reinterpret_cast<const __half *>(rec + off)[i]);
-        };
-        if (kv == 0) {
-            q4_codes(rec, 0, d, rp, [&](int k, int n, float c) { Rs[n * d + k] = c * sc(y.q_off_sRK, q4_dscale_index(k)); });
-            q4_codes(rec, q4_operand_regs(d, rp), rp, P,
-                     [&](int k, int n, float c) { Ls[n * rp + k] = c * sc(y.q_off_sLK, q4_scale_index(rp, k)); });
-        } else {
-            const char *vs = rec + y.q_off_V;
-            q4_codes(vs, 0, P, rp, [&](int k, int n, float c) { Ls[k * rp + n] = c * sc(y.q_off_sLV, q4_scale_index(P, k)); });
-            q4_codes(vs, q4_operand_regs(P, rp), rp, d,
-                     [&](int k, int n, float c) { Rs[k * d + n] = c * sc(y.q_off_sRV, q4_dscale_index(n)); });
-        }
-        return;
-    }
-    if (kv == 0) {
-        for (int e = threadIdx.x; e < P * rp; e += blockDim.x) Ls[e] = Elem<T>::load(swz_ptr<T>(rec, e / rp, e % rp, rp));
-        for (int e = threadIdx.x; e < rp * d; e += blockDim.x)
-            Rs[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_RK, e / d, e % d, d));
-    } else {
-        for (int e = threadIdx.x; e < P * rp; e += blockDim.x)
-            Ls[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_LV, e % rp, e / rp, P));
-        for (int e = threadIdx.x; e < rp * d; e += blockDim.x)
-            Rs[e] = Elem<T>::load(swz_ptr<T>(rec + y.off_RV, e % d, e / d, rp));
-    }
-}
-
 // Block (page of a call entry, head, K/V): the page's rows inside the entry's
-// range.  Each thread holds columns c and c + d/2 of its rows, the pair that
-// RoPE turns together.
+// range, a thread to 16 bytes of a row.  fp32 factorized pages are rebuilt as L
+// R in fp32; bf16 calls take dense and chunk rows only (read_kernel rebuilds).
 template <typename T>
 __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
     extern __shared__ __align__(128) unsigned char sm[];
+    constexpr int VE = 16 / sizeof(T);  // elements of a thread
     const Layout &y = p.y;
     const int P = y.P, d = y.d, h = blockIdx.y, kv = blockIdx.z;
     int i = 0;
@@ -72,64 +24,52 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
     const int lo = p.lo[i], hi = lo + p.n[i], T0 = p.T[i], b = p.seqs[i];
     const int pg = lo / P + (int)blockIdx.x - p.page_off[i];
     const int r0 = max(lo, pg * P), r1 = min(hi, pg * P + P);
-    const bool cached = pg * P < T0;
-    const bool factored = cached && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
+    const bool factored = pg * P < T0 && page_kind(pg, T0, P, y.sink_tokens, y.W) == KIND_FACTORED;
     const int rp = kv == 0 ? y.rkp : y.rvp;
-    float *Ls = reinterpret_cast<float *>(sm), *Rs = Ls + P * rp;
-    const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, kv);
-    if (factored) {
-        load_page_factors<T>(y, p.factor_pool + y.record_offset(p.layer, b, h, pg), kv, Ls, Rs);
-        __syncthreads();
+    float *Ls = reinterpret_cast<float *>(sm), *Rs = Ls + P * rp;  // L [P][rp], R [rp][d]
+    if constexpr (sizeof(T) == 4) {
+        if (factored) {
+            const char *rec = p.factor_pool + y.record_offset(p.layer, b, h, pg);
+            for (int e = threadIdx.x; e < P * rp; e += blockDim.x)
+                Ls[e] = kv == 0 ? *swz_ptr<float>(rec, e / rp, e % rp, rp) : *swz_ptr<float>(rec + y.off_LV, e % rp, e / rp, P);
+            for (int e = threadIdx.x; e < rp * d; e += blockDim.x)
+                Rs[e] = kv == 0 ? *swz_ptr<float>(rec + y.off_RK, e / d, e % d, d)
+                                : *swz_ptr<float>(rec + y.off_RV, e % d, e / d, rp);
+            __syncthreads();
+        }
     }
+    const char *page = p.dense_pool + y.dense_offset(p.layer, b, y.dense_slot(pg), h, kv);
     const T *chunk = reinterpret_cast<const T *>(kv == 0 ? p.k_new : p.v_new);
     T *out = reinterpret_cast<T *>(kv == 0 ? p.k_out : p.v_out);
-    const int half = d / 2, c = threadIdx.x % half, step = blockDim.x / half;
-    const bool turn = kv == 0 && y.rope && p.turn;
-    for (int r = r0 + threadIdx.x / half; r < r1; r += step) {
-        const int t = r - pg * P;
-        T x0, x1;
-        float f0 = 0.f, f1 = 0.f;
+    const int nv = d / VE;
+    for (int e = threadIdx.x; e < (r1 - r0) * nv; e += blockDim.x) {
+        const int r = r0 + e / nv, c = e % nv * VE, t = r - pg * P;
+        uint4 x;
         if (factored) {
-            for (int j = 0; j < rp; ++j) {
-                const float l = Ls[t * rp + j];
-                f0 = fmaf(l, Rs[j * d + c], f0);
-                f1 = fmaf(l, Rs[j * d + c + half], f1);
-            }
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (sizeof(T) == 4)
+                for (int j = 0; j < rp; ++j) {
+                    const float l = Ls[t * rp + j];
+                    const float4 v = *reinterpret_cast<const float4 *>(Rs + j * d + c);
+                    f = make_float4(fmaf(l, v.x, f.x), fmaf(l, v.y, f.y), fmaf(l, v.z, f.z), fmaf(l, v.w, f.w));
+                }
+            x = make_uint4(__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z), __float_as_uint(f.w));
+        } else if (r < T0) {
+            x = *reinterpret_cast<const uint4 *>(swz_ptr<T>(page, t, c, d));
         } else {
-            if (r < T0) {
-                x0 = *swz_ptr<T>(page, t, c, d);
-                x1 = *swz_ptr<T>(page, t, c + half, d);
-            } else {
-                const T *src = chunk + ((size_t)(p.coff[i] + r - T0) * y.H + h) * d;
-                x0 = src[c];
-                x1 = src[c + half];
-            }
-            f0 = Elem<T>::load(&x0);
-            f1 = Elem<T>::load(&x1);
+            x = *reinterpret_cast<const uint4 *>(chunk + ((size_t)(p.coff[i] + r - T0) * y.H + h) * d + c);
         }
-        if (turn) {  // position pg P + t: the page start's angle plus the offset's
-            const float2 a = p.rope_base[(size_t)pg * half + c], o = p.rope_delta[t * half + c];
-            const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
-            const float u0 = f0 * cs - f1 * sn, u1 = f1 * cs + f0 * sn;
-            f0 = u0;
-            f1 = u1;
-        }
-        if (factored || turn) {
-            x0 = Elem<T>::from_f32(f0);
-            x1 = Elem<T>::from_f32(f1);
-        }
-        T *dst = out + (size_t)(p.off[i] + r - lo) * p.row_stride + (size_t)h * p.head_stride;
-        dst[c] = x0;
-        dst[c + half] = x1;
+        *reinterpret_cast<uint4 *>(out + (size_t)(p.off[i] + r - lo) * p.row_stride + (size_t)h * p.head_stride + c) = x;
     }
 }
 
-// The same for bf16 factors (no chunk rows), HBM-bound: a factorized row is 0.47
-// of its bytes as factors, and all of them are written.  CTAs stay and loop over
-// items (128 positions of an entry, head, K/V): the next item's factors arrive
-// while one is computed on the warps' tensor cores (fp32 sums, rounded once) and
-// written a whole row per sixteen lanes.  32K tokens x 8 heads, ranks 16 and 24:
-// 0.28 ms with the scalar products of rows_kernel.
+// Rows of bf16 stores, HBM-bound: a factorized row is 0.47 of its bytes as
+// factors, and all of them are written.  CTAs stay and loop over items (128
+// positions of an entry, head, K/V): the next item's factors arrive while one is
+// computed on the warps' tensor cores (fp32 sums, rounded once) and written a
+// whole row per sixteen lanes.  32K tokens x 8 heads, ranks 16 and 24: 52 us (3.8
+// TB/s; 277 us with scalar products, a block per page); a CTA's item is a chain of
+// short steps, and two CTAs of 16 warps fill the registers.
 struct ReadItem {
     int i, b, h, kv, pg0, lo, hi, off, fw;
     ReadItem() = default;
