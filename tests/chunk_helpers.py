@@ -12,7 +12,8 @@ import oracle
 from gpu_helpers import HostCache
 from store_layout import Layout, factor_pool_slice, read_factors
 
-U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}  # half a step, relative
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}  # half a step, relative: outputs and rows
+U_IN = {torch.bfloat16: 2.0 ** -11, torch.float32: 2.0 ** -24}  # of rebuilt operands and weights (fp16 for bf16 stores)
 U32 = 2.0 ** -24
 
 
@@ -67,17 +68,20 @@ def pair_abs(Xa, theta):
     return np.concatenate([s, s], -1)
 
 
-def chunk_reference(cfg, rows, k, v, q, T):
+def chunk_reference(cfg, rows, k, v, q, T, u_in=None):
     """64-bit attention of one sequence's chunk and its error bound.
 
     rows: cache_rows at length T; k, v [n, H, d], q [n, Hq, d] torch tensors.
-    The bound: with u the half step of kv_dtype, a key is off by u |k| (one
-    rounding of the rebuilt row) plus (rank + 20) U32 |L||R| (fp32 products and
-    angles), so a score is off by at most ds = (u + (d + rank + 20) U32) A, A =
-    max over seen keys of sum |q||k| / sqrt(d); a weight, normalised, by the
-    factor e^(2 ds); the weight's own rounding (u) and the value's (u, and its
-    fp32 products) enter linearly, sums of T weights as T U32, and the output is
-    rounded once (u |o|).  U32 terms also cover exp2 (2^-22)."""
+    The bound: with ui the half step of the operands (fp16 in bf16 stores, which
+    the few-token path's split operands keep as well) and u that of the output, a
+    key is off by ui |k| (one rounding of the rebuilt row), the query by ui |q|,
+    plus (rank + 20) U32 |L||R| (fp32 products and angles), so a score is off by
+    at most ds = (2 ui + (d + rank + 20) U32) A, A = max over seen keys of sum
+    |q||k| / sqrt(d); a weight, normalised, by the factor e^(2 ds); the weight's
+    own rounding and the value's (ui each, and its fp32 products) enter linearly,
+    sums of T weights as T U32, and the output is rounded once (u |o|).  U32
+    terms also cover exp2 (2^-22).  Below fp16's normal range a weight or a value
+    is off by 2^-25 absolute."""
     K, V, Ka, Va = rows
     H, G, d, n = cfg.num_kv_heads, cfg.num_q_heads // cfg.num_kv_heads, cfg.head_dim, q.shape[0]
     theta = float(cfg.rope_theta)
@@ -90,6 +94,8 @@ def chunk_reference(cfg, rows, k, v, q, T):
     K = turned(K, 0, theta)
     qn = q.double().cpu().numpy()
     u = U[cfg.kv_dtype]
+    ui = U_IN[cfg.kv_dtype] if u_in is None else u_in
+    tiny = 2.0 ** -25 if cfg.kv_dtype == torch.bfloat16 else 0.0
     rank = max(cfg.rank_k, cfg.rank_v)
     out, bound = np.zeros((n, H * G, d)), np.zeros((n, H * G, d))
     for j in range(n):
@@ -102,9 +108,11 @@ def chunk_reference(cfg, rows, k, v, q, T):
             w /= w.sum(1, keepdims=True)
             o = w @ V[h, :see]
             B = w @ Va[h, :see]
-            ds = (u + (d + rank + 20) * U32) * A
+            ds = (2 * ui + (d + rank + 20) * U32) * A
             out[j, h * G:(h + 1) * G] = o
-            bound[j, h * G:(h + 1) * G] = (np.expm1(2 * ds) + 2.05 * u + (see + rank + 40) * U32) * B + u * np.abs(o)
+            inner = ((np.expm1(2 * ds) + 2.05 * ui + (see + rank + 40) * U32) * B +
+                     tiny * (1 + see * np.abs(V[h, :see]).max(0, keepdims=True)))
+            bound[j, h * G:(h + 1) * G] = inner + u * (np.abs(o) + inner)
     return out, bound
 
 
