@@ -315,8 +315,9 @@ class Store:
         return torch.cuda.device(self._index)
 
     def _queue(self, stream) -> ctypes.c_void_p:
-        s = stream if stream is not None else torch.cuda.current_stream(self._index)
-        return ctypes.c_void_p(s.cuda_stream)
+        # the raw handle alone: making a Stream object takes longer than a small launch
+        return ctypes.c_void_p(stream.cuda_stream if stream is not None
+                               else torch._C._cuda_getCurrentRawStream(self._index))
 
     def _need_here(self, t: torch.Tensor, shape, name: str) -> None:
         _need(t, shape, self.cfg.kv_dtype, name)
@@ -397,8 +398,8 @@ class Store:
         N = sum(cnt[:B])
         with self._on(stream):
             # one row at least, so that an empty read still has a pointer
-            kv = torch.empty(2, max(N, 1), c.num_kv_heads, c.head_dim, dtype=c.kv_dtype, device=self.dense_pool.device)
-            k, v = kv.unbind(0)
+            k = torch.empty((max(N, 1), c.num_kv_heads, c.head_dim), dtype=c.kv_dtype, device=self.dense_pool.device)
+            v = torch.empty_like(k)
             check(lib().puzzlekv_read_tokens(self._h, layer, ids, st, cnt, B, _ptr(k), _ptr(v), self._queue(stream)))
         return (k, v) if N else (k[:0], v[:0])
 
