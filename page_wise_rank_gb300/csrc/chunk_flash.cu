@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         mbar_init(&bars[1], 1);
         fence_barrier_init();
     }
+    grid_dependency_wait();  // the launch before may still write pages, or read the images
     __syncthreads();
     auto buffer = [&](int buf) { return sm + IMG + buf * NP * bl.fetch_bytes; };
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
@@ -715,8 +716,7 @@ static cudaError_t stage_t(const StageParams &p, int num_sms, cudaStream_t st) {
     cudaError_t e = allow_smem<stage_kernel<P, D, Q4>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.blk_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    stage_kernel<P, D, Q4><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(stage_kernel<P, D, Q4>, dim3((unsigned)std::min(items, num_sms * resident)), STAGE_THREADS, smem, st, p);
 }
 
 cudaError_t launch_stage(const StageParams &p, int num_sms, cudaStream_t st) {

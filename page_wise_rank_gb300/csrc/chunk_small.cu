@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
         sh.failed = 0;
         fence_barrier_init();
     }
+    grid_dependency_wait();  // the launch before may still write pages or queries
     __syncthreads();
     const int slot0 = pg * SPG;
     const bool active = pg < PG, leader = active && rt == 0 && lane == 0;
@@ -518,8 +519,8 @@ template <int P, int D>
 static cudaError_t small_t(const SmallParams &p, size_t smem, cudaStream_t st) {
     cudaError_t e = allow_smem<small_kernel<P, D>>(smem);
     if (e != cudaSuccess) return e;
-    small_kernel<P, D><<<dim3((unsigned)(p.boff[p.nseq] - p.nseq), (unsigned)p.y.H), 32 * SMALL_WARPS, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(small_kernel<P, D>, dim3((unsigned)(p.boff[p.nseq] - p.nseq), (unsigned)p.y.H), 32 * SMALL_WARPS, smem,
+                            st, p);
 }
 
 cudaError_t launch_small(SmallParams &p, cudaStream_t st) {

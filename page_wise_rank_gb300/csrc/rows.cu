@@ -104,6 +104,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
         mbar_init(&bars[1], 1);
         fence_barrier_init();
     }
+    grid_dependency_wait();  // the launch before may still write pages
     __syncthreads();
     auto buffer = [&](int buf) { return sm + TILE + buf * NP * bl.fetch_bytes; };
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
@@ -253,8 +254,7 @@ static cudaError_t read_t(const RowsParams &p, int num_sms, cudaStream_t st) {
     cudaError_t e = allow_smem<read_kernel<P, D, Q4>>(smem);
     if (e != cudaSuccess) return e;
     const int items = 2 * p.page_off[p.nseq] * p.y.H, resident = std::min(2, 227 * 1024 / (smem + 1024));
-    read_kernel<P, D, Q4><<<(unsigned)std::min(items, num_sms * resident), STAGE_THREADS, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(read_kernel<P, D, Q4>, dim3((unsigned)std::min(items, num_sms * resident)), STAGE_THREADS, smem, st, p);
 }
 
 cudaError_t launch_read(RowsParams &p, int num_sms, cudaStream_t st) {
