@@ -347,6 +347,14 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
 // while one tile's softmax runs, the other tile's two products do.  A commit
 // covers every product issued before it: when a tile's S is complete, so is
 // its previous P V, and its threads may rescale O.
+//
+// Bound by the softmax and the products together: a unit of 2 x 128 x 128 takes
+// 3,180 cycles, its products 2,048, each tile's softmax 1,550 (exponentials and
+// packing 975 of them).  2,048 tokens over 30K, 32 / 8 heads: 670 us, 1.6 PFLOP/s,
+// tensor cores active 70 %.  Slower: two threads to a row (the exchange of maxima
+// costs what the halves save), a warp per tile for the products (they interleave),
+// a share of the exponentials as polynomials (the special-function unit is not the
+// bound).
 template <int D>
 __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashParams p) {
     extern __shared__ unsigned char sm_raw[];
@@ -554,79 +562,79 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
             }
         }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-      if (warp == 8) {
-        // One elected lane issues, but the whole warp runs the loop: addresses
-        // and descriptors then stay in uniform registers.  With a single lane
-        // in the loop each product took 90-107 cycles to issue against the 64
-        // it runs for.
-        const uint32_t leader = elect_one();
-        const uint64_t dq = tc_desc(smem_u32(Qs)), dr = tc_desc(smem_u32(ring));
-        constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
-        uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, role_wait(s, bar, parity, p.status)) != 0; };
-        auto full = [&](uint32_t n) { return wait(&s.kv_full[n % RING], (n / RING) & 1); };
-        auto scores = [&](int t, uint32_t n) {
-            const uint64_t a = dq + t * (IMG >> 4), b = dr + (n % RING) * (IMG >> 4);
-            if (leader) {
+        // One instruction for the whole warpgroup, before its warps part.
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 8) {
+            // One elected lane issues, but the whole warp runs the loop: addresses
+            // and descriptors then stay in uniform registers.  With a single lane
+            // in the loop each product took 90-107 cycles to issue against the 64
+            // it runs for.
+            const uint32_t leader = elect_one();
+            const uint64_t dq = tc_desc(smem_u32(Qs)), dr = tc_desc(smem_u32(ring));
+            constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
+            uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, role_wait(s, bar, parity, p.status)) != 0; };
+            auto full = [&](uint32_t n) { return wait(&s.kv_full[n % RING], (n / RING) & 1); };
+            auto scores = [&](int t, uint32_t n) {
+                const uint64_t a = dq + t * (IMG >> 4), b = dr + (n % RING) * (IMG >> 4);
+                if (leader) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc_mma_ss(tmem + 128 * t, a + (k / 4) * (128 * 128 >> 4) + (k % 4) * 2,
-                              b + (k / 4) * (FLASH_KEYS * 128 >> 4) + (k % 4) * 2, ID_S, k > 0);
-                tc_commit(&s.s_full[t]);
-            }
-            __syncwarp();
-        };
-        auto values = [&](int t, uint32_t n, bool acc) {
-            const uint64_t b = dr + (n % RING) * (IMG >> 4);
-            if (leader) {
-#pragma unroll
-                for (int k = 0; k < FLASH_KEYS / 16; ++k)
-                    tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + (k / 4) * (D * 128 >> 4) + (k % 4) * 2, ID_O,
-                              acc || k > 0);
-            }
-            __syncwarp();
-        };
-        auto commit = [&](uint64_t *bar) {
-            if (leader) tc_commit(bar);
-            __syncwarp();
-        };
-        while (ok && pc.next()) {
-            const int tiles = pc.cpair * FLASH_ROWS + 128 < pc.rows() ? 2 : 1, nb = pc.cb1 - pc.cb0;
-            for (int t = 0; t < tiles && ok; ++t) {
-                ok = wait(&s.q_full[t], q_phase[t]);
-                q_phase[t] ^= 1;
-            }
-            ok = ok && full(x);
-            if (!ok) break;
-            tc_fence_after();
-            for (int t = 0; t < tiles; ++t) scores(t, x);
-            commit(&s.kv_empty[x % RING]);
-            for (int j = 0; j < nb && ok; ++j) {
-                const uint32_t v = x + 1 + 2 * j;
-                const bool more = j + 1 < nb;
-                ok = full(v) && (!more || full(v + 1));
-                for (int t = 0; t < tiles && ok; ++t) {
-                    ok = wait(&s.p_full[t], p_phase[t]);
-                    if (!ok) break;
-                    p_phase[t] ^= 1;
-                    tc_fence_after();
-                    values(t, v, j > 0);
-                    if (more)
-                        scores(t, v + 1);
-                    else
-                        commit(&s.o_full[t]);
+                    for (int k = 0; k < D / 16; ++k)
+                        tc_mma_ss(tmem + 128 * t, a + (k / 4) * (128 * 128 >> 4) + (k % 4) * 2,
+                                  b + (k / 4) * (FLASH_KEYS * 128 >> 4) + (k % 4) * 2, ID_S, k > 0);
+                    tc_commit(&s.s_full[t]);
                 }
-                commit(&s.kv_empty[v % RING]);
-                if (more) commit(&s.kv_empty[(v + 1) % RING]);
+                __syncwarp();
+            };
+            auto values = [&](int t, uint32_t n, bool acc) {
+                const uint64_t b = dr + (n % RING) * (IMG >> 4);
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < FLASH_KEYS / 16; ++k)
+                        tc_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + (k / 4) * (D * 128 >> 4) + (k % 4) * 2, ID_O,
+                                  acc || k > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t *bar) {
+                if (leader) tc_commit(bar);
+                __syncwarp();
+            };
+            while (ok && pc.next()) {
+                const int tiles = pc.cpair * FLASH_ROWS + 128 < pc.rows() ? 2 : 1, nb = pc.cb1 - pc.cb0;
+                for (int t = 0; t < tiles && ok; ++t) {
+                    ok = wait(&s.q_full[t], q_phase[t]);
+                    q_phase[t] ^= 1;
+                }
+                ok = ok && full(x);
+                if (!ok) break;
+                tc_fence_after();
+                for (int t = 0; t < tiles; ++t) scores(t, x);
+                commit(&s.kv_empty[x % RING]);
+                for (int j = 0; j < nb && ok; ++j) {
+                    const uint32_t v = x + 1 + 2 * j;
+                    const bool more = j + 1 < nb;
+                    ok = full(v) && (!more || full(v + 1));
+                    for (int t = 0; t < tiles && ok; ++t) {
+                        ok = wait(&s.p_full[t], p_phase[t]);
+                        if (!ok) break;
+                        p_phase[t] ^= 1;
+                        tc_fence_after();
+                        values(t, v, j > 0);
+                        if (more)
+                            scores(t, v + 1);
+                        else
+                            commit(&s.o_full[t]);
+                    }
+                    commit(&s.kv_empty[v % RING]);
+                    if (more) commit(&s.kv_empty[(v + 1) % RING]);
+                }
+                x += 2 * nb;
             }
-            x += 2 * nb;
-        }
-        if (!ok)  // products still in flight end before the tensor memory is freed
-            for (int k = 0; k < 1000; ++k) __nanosleep(1000);
-      } else if (warp == 9) {
-        if (lane == 0) {
+            if (!ok)  // products still in flight end before the tensor memory is freed
+                for (int k = 0; k < 1000; ++k) __nanosleep(1000);
+        } else if (warp == 9 && lane == 0) {
             uint32_t x = 0;
             bool ok = true;
             while (ok && pc.next()) {
@@ -642,7 +650,6 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 for (uint32_t k = x < RING ? 0 : x - RING; k < x; ++k)
                     mbar_wait_bounded(&s.kv_full[k % RING], (k / RING) & 1, nullptr);
         }
-      }
     }
     __syncwarp();
     tc_fence_before();
@@ -652,7 +659,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
 }
 
 // Join the states of the pairs cut between CTAs, eq. (5).  Block (boundary,
-// group of 32 rows): the boundary of shares c and c + 1, if it cuts a pair and is
+// group of 8 rows): the boundary of shares c and c + 1, if it cuts a pair and is
 // the first that does; one warp per row, the pieces' o summed in order, the same in
 // every launch.
 template <int D>
