@@ -778,6 +778,8 @@ puzzlekv_status puzzlekv_truncate_sequences(puzzlekv_store *s, const int32_t *se
                     s->dense_lo[x] = y.sink_pages;
                     continue;
                 }
+                // pages from the cut on are written anew: they will be in the ring
+                s->dense_lo[x] = std::min(s->dense_lo[x], std::max(y.sink_pages, complete));
                 // a page cut into is filled again with other tokens: its factors are void
                 s->conv_upto[x] = std::max(y.sink_pages, std::min(s->conv_upto[x], complete));
                 std::vector<uint8_t> &m = s->marked[x];

@@ -139,6 +139,36 @@ def test_cut_too_far_is_refused(pkv):
     check_page_table(store, cfg, 0, 0, 63)
 
 
+@pytest.mark.parametrize("name,T", [("llama", 40), ("llama", 64), ("p32", 9), ("nosink-nowindow", 320), ("fp32", 16)])
+def test_grown_again_after_a_long_cut(pkv, name, T):
+    """A cut that leaves no dense page past the sink (the ring has moved on): pages filled afterwards are in the ring,
+    so they are copied and can be cut into like any others."""
+    cfg = make_cfg(pkv, **STORES[name])
+    P = cfg.page_size
+    store, _ = filled(pkv, cfg, [900, 0, 0, 0])
+    fresh, _ = filled(pkv, cfg, [900, 0, 0, 0])
+    n = 2 * P + 3
+    for layer in range(cfg.num_layers):
+        k, v = (x.cuda() for x in random_rows(cfg, 300, 6 + layer))
+        store.append_chunk(layer, k, v, [0], [300])
+    for s in (store, fresh):  # `fresh` is cut without having grown
+        s.truncate_sequences([0], [T])
+        for layer in range(cfg.num_layers):
+            k, v = (x.cuda() for x in random_rows(cfg, n, 60 + layer))
+            s.append_chunk(layer, k, v, [0], [n])
+        s.copy_sequences([0, 0], [1, 2])
+        s.truncate_sequences([0, 2], [T + n - 2, T + n - 2])
+    for layer in range(cfg.num_layers):
+        cut = live_state(store, cfg, 0, layer)
+        same_state(cut, live_state(store, cfg, 2, layer))
+        same_state(cut, live_state(fresh, cfg, 0, layer))
+        same_state(live_state(store, cfg, 1, layer), live_state(fresh, cfg, 1, layer))
+        k1, v1 = store.read_tokens(layer, [1], [0], [T + n - 2])
+        k0, v0 = store.read_tokens(layer, [0], [0], [T + n - 2])
+        lo = max(0, T + n - 2 - P)  # the rows of the last pages are dense at both lengths
+        assert torch.equal(k1[lo:], k0[lo:]) and torch.equal(v1[lo:], v0[lo:])
+
+
 def test_serving_run(pkv):
     """A prompt in chunks, forked, drafts verified, some rejected, beams reordered, single tokens decoded: every answer
     against 64 bits."""
