@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
             reinterpret_cast<float *>(p.scales)[item] = (float)scale;
         }
     }
-    if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the images are written
 }
 
 // ---------------------------------------------------------------- attention

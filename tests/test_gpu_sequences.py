@@ -169,6 +169,44 @@ def test_grown_again_after_a_long_cut(pkv, name, T):
         assert torch.equal(k1[lo:], k0[lo:]) and torch.equal(v1[lo:], v0[lo:])
 
 
+def test_offsets_past_32_bits(pkv):
+    """Long sequences whose records and operand images lie more than 4 GiB into their buffers: the same rows as a
+    store of one sequence, and the same attention.  The two calls share their operands but cut the keys in other
+    places, so weights and states round differently (2^-11 of sum w |v| each, at most max |v| = 2^-11 * 8 here) and both
+    outputs round once (2^-8 of the value each)."""
+    T, n, last = 131000, 70, 17
+    base = dict(num_layers=1, num_kv_heads=8, num_q_heads=32, max_tokens_per_seq=131072)
+    big, one = pkv.Store(make_cfg(pkv, max_batch=last + 1, **base)), pkv.Store(make_cfg(pkv, max_batch=1, **base))
+    assert big.factor_pool.numel() > 1 << 32
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *shape: (0.6 * torch.randn(shape, generator=g, device="cuda")).clamp(-4, 4).bfloat16()
+    K, V = rnd(1, 8, T, 128), rnd(1, 8, T, 128)
+    big.load_prefill(0, K, V)
+    big.copy_sequences([0] * (last - 1), list(range(1, last)))
+    V += 2  # the last sequence's outputs are near 2, the others' near 0
+    big.load_prefill(last, K, V)
+    one.load_prefill(0, K, V)
+    for start in (0, T - 500):
+        for x, y in zip(big.read_tokens(0, [last], [start], [500]), one.read_tokens(0, [0], [start], [500])):
+            assert torch.equal(x, y)
+    for x, y in zip(big.read_tokens(0, [last - 1], [64], [500]), big.read_tokens(0, [0], [64], [500])):
+        assert torch.equal(x, y)
+    q, k, v = rnd(n, 32, 128), rnd(n, 8, 128), rnd(n, 8, 128) + 2
+    ids = list(range(8, last + 1))
+    assert big.chunk_workspace(0, ids, [n] * len(ids))["attention"] > 1 << 32
+    got = big.chunk_attention(0, *(x.repeat(len(ids), 1, 1) for x in (q, k, v)), ids, [n] * len(ids))[-n:]
+    want = one.chunk_attention(0, q, k, v, [0], [n])
+    few = [s.chunk_attention(0, q[:4], k[:4], v[:4], [b], [4]) for s, b in ((big, last), (one, 0))]  # over the pages
+    for a, b in ((got, want), few):
+        assert ((a.float() - b.float()).abs() <= 2.0 ** -7 * b.float().abs() + 2 * 2.0 ** -11 * 8).all()
+    assert want.float().mean() > 1.5
+    big.append_chunk(0, k, v, [last], [n])
+    one.append_chunk(0, k, v, [0], [n])
+    for x, y in zip(big.read_tokens(0, [last], [T - 300], [300 + n]), one.read_tokens(0, [0], [T - 300], [300 + n])):
+        assert torch.equal(x, y)
+    assert big.check_device_status() == 0
+
+
 def test_serving_run(pkv):
     """A prompt in chunks, forked, drafts verified, some rejected, beams reordered, single tokens decoded: every answer
     against 64 bits."""
