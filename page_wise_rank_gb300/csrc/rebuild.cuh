@@ -66,34 +66,46 @@ struct BlockPages {
             if (Q4) bulk_g2s(buf + s * bl.fetch_bytes + bl.scales, src + y.q_off_sRK, tail, bar);
         }
     }
-    // INT4: the factorized pages' matrices from their codes.  All threads; a barrier follows.
+    // INT4: the factorized pages' matrices from their codes, a warp to a slab of
+    // eight registers per lane.  All threads; a barrier follows.
     __device__ __forceinline__ void expand(const Layout &y, const BlockLayout &bl, int kv, const unsigned char *buf,
                                            unsigned char *pages) const {
-        const int K1 = kv ? y.P : y.d, r = kv ? y.rvp : y.rkp, K2 = r, N2 = kv ? y.d : y.P;
-        const int n1 = q4_operand_regs(K1, r), n = n1 + q4_operand_regs(K2, N2);
-        for (int e = threadIdx.x; e < (hi - lo) * n * 32; e += blockDim.x) {
-            const int s = lo + e / (n * 32), m = e / 32 % n, lane = e % 32, w = m / 4;
+        const int K1 = kv ? y.P : y.d, r = kv ? y.rvp : y.rkp, N2 = kv ? y.d : y.P;
+        const int n1 = q4_operand_regs(K1, r), n = n1 + q4_operand_regs(r, N2), slabs = (n + 7) / 8;
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        // registers of a 16-wide k-step, and their reciprocals (exact for the few hundred registers there are)
+        const int step1 = r / 4, step2 = N2 / 4;
+        const uint32_t inv1 = (65536 + step1 - 1) / step1, inv2 = (65536 + step2 - 1) / step2;
+        // R_K [dim][rank] -> RK[rank][dim], L_V [token][rank] -> LVt[rank][token]
+        const SwzRows first((kv ? 0u : bl.kR) + 4 * c, g, K1 * 2);
+        // L_K [rank][token] -> LK[token][rank], R_V [rank][dim] -> RVt[dim][rank]
+        const SwzRows second((kv ? bl.vR : 0u) + 4 * c, g, r * 2);
+        for (int u = threadIdx.x >> 5; u < (hi - lo) * slabs; u += STAGE_THREADS / 32) {
+            int s = lo, slab = u;
+            for (; slab >= slabs; slab -= slabs) ++s;
             const unsigned char *src = buf + s * bl.fetch_bytes;
             unsigned char *dst = pages + s * bl.page_bytes;
-            const uint32_t word = *reinterpret_cast<const uint32_t *>(src + ((w / 2) * 32 + lane) * 8 + (w % 2) * 4);
-            // nibbles m % 4 and m % 4 + 4: elements (k, n) and (k + 1, n)
-            const float c0 = (float)((int)((word >> (4 * (m % 4))) & 15u) - 8), c1 = (float)((int)((word >> (4 * (m % 4) + 16)) & 15u) - 8);
-            int k, col;
-            if (m < n1) {  // R_K [dim][rank] -> RK[rank][dim];  L_V [token][rank] -> LVt[rank][token]
-                q4_operand_elem(K1, r, m, lane, 0, k, col);
-                *reinterpret_cast<uint32_t *>(dst + (kv ? 0u : bl.kR) + swz_offset(col, 2 * k, K1 * 2)) = pack_f16(c0, c1);
-            } else {  // L_K [rank][token] -> LK[token][rank];  R_V [rank][dim] -> RVt[dim][rank]
-                q4_operand_elem(K2, N2, m - n1, lane, 0, k, col);
-                const uint32_t at = swz_offset(col, 2 * k, r * 2);
-                if (kv) {
-                    *reinterpret_cast<uint32_t *>(dst + bl.vR + at) = pack_f16(c0, c1);
+            const uint2 words = *reinterpret_cast<const uint2 *>(src + (slab * 32 + lane) * 8);
+            const uint32_t *sLK =
+                reinterpret_cast<const uint32_t *>(src + bl.scales + (y.q_off_sLK - y.q_off_sRK)) + c * (r / 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int m = 8 * slab + j;
+                if (m >= n) break;
+                const uint32_t x = q4_reg(j < 4 ? words.x : words.y, j & 3);
+                const bool one = m < n1;
+                const int k = one ? m : m - n1, ks = (int)((k * (one ? inv1 : inv2)) >> 16), rem = k - ks * (one ? step1 : step2);
+                const bool wide = 16 * ks + 16 <= (one ? K1 : r);  // else the last step, eight wide
+                const int tile = wide ? rem >> 1 : rem, chunk = 2 * ks + (wide ? rem & 1 : 0);
+                if (one) {
+                    *reinterpret_cast<uint32_t *>(dst + first(tile, chunk)) = x;
+                } else if (kv) {
+                    *reinterpret_cast<uint32_t *>(dst + second(tile, chunk)) = x;
                 } else {
-                    const __half *sLK = reinterpret_cast<const __half *>(src + bl.scales + (y.q_off_sLK - y.q_off_sRK));
                     uint32_t hi16, lo16;
-                    split_f16(c0 * __half2float(sLK[q4_scale_index(r, k)]), c1 * __half2float(sLK[q4_scale_index(r, k + 1)]), hi16,
-                              lo16);
-                    *reinterpret_cast<uint32_t *>(dst + at) = hi16;
-                    *reinterpret_cast<uint32_t *>(dst + y.P * r * 2 + at) = lo16;
+                    mul_split_f16(x, sLK[chunk], hi16, lo16);
+                    *reinterpret_cast<uint32_t *>(dst + second(tile, chunk)) = hi16;
+                    *reinterpret_cast<uint32_t *>(dst + y.P * r * 2 + second(tile, chunk)) = lo16;
                 }
             }
         }
@@ -246,23 +258,24 @@ struct RowTile {
     // Turn keys stored before RoPE by their positions pg P + t0 + row (the page
     // start's angle plus the offset's); rows at positions T1 and past are zeros.
     __device__ __forceinline__ void turn(float (&acc)[8][4], const float2 *rope_base, const float2 *rope_delta, int pg, int T1) const {
+        if (pg * P + t0 >= T1) return;  // perhaps past the tables
         const int g = lane >> 2, c = lane & 3;
 #pragma unroll
-        for (int r2 = 0; r2 < 2; ++r2) {
-            const int t = t0 + g + 8 * r2;
-            if (pg * P + t >= T1) continue;
+        for (int j = 0; j < KT / 2; ++j) {
+            const int i = 8 * nt(j) + 2 * c;  // angles i and i + 1
+            const float4 a = *reinterpret_cast<const float4 *>(rope_base + (size_t)pg * (D / 2) + i);
 #pragma unroll
-            for (int j = 0; j < KT / 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 8 * nt(j) + 2 * c + e;
-                    const float2 a = rope_base[(size_t)pg * (D / 2) + i], o = rope_delta[t * (D / 2) + i];
-                    const float cs = a.x * o.x - a.y * o.y, sn = a.y * o.x + a.x * o.y;
-                    float &x0 = acc[j][2 * r2 + e], &x1 = acc[j + KT / 2][2 * r2 + e];
+            for (int r2 = 0; r2 < 2; ++r2) {
+                const float4 o = *reinterpret_cast<const float4 *>(rope_delta + (t0 + g + 8 * r2) * (D / 2) + i);
+                auto one = [&](float ax, float ay, float ox, float oy, float &x0, float &x1) {
+                    const float cs = ax * ox - ay * oy, sn = ay * ox + ax * oy;
                     const float u0 = x0 * cs - x1 * sn, u1 = x1 * cs + x0 * sn;
                     x0 = u0;
                     x1 = u1;
-                }
+                };
+                one(a.x, a.y, o.x, o.y, acc[j][2 * r2], acc[j + KT / 2][2 * r2]);
+                one(a.z, a.w, o.z, o.w, acc[j][2 * r2 + 1], acc[j + KT / 2][2 * r2 + 1]);
+            }
         }
     }
 };
