@@ -293,12 +293,18 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                         }
                     }
                     if (Q4) {
-                        const float dim[2] = {bp.dim_scale(y, bl, buffer(buf), s, 1, d0 + g), bp.dim_scale(y, bl, buffer(buf), s, 1, d0 + g + 8)};
+                        float dim[2];
+                        for (int r2 = 0; r2 < 2; ++r2) {
+                            const int n = d0 + g + 8 * r2;
+                            const float2 f = bp.dim_scales(y, bl, buffer(buf), s, 1, n & ~1);
+                            dim[r2] = n & 1 ? f.y : f.x;
+                        }
 #pragma unroll
-                        for (int j = 0; j < PT; ++j)
+                        for (int j = 0; j < PT; ++j) {
+                            const float2 f = bp.token_scales(y, bl, buffer(buf), s, off + 8 * j + 2 * c);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[s2 * PT + j][e] *= dim[e >> 1] * bp.token_scale(y, bl, buffer(buf), s, off + 8 * j + 2 * c + (e & 1));
+                            for (int e = 0; e < 4; ++e) acc[s2 * PT + j][e] *= dim[e >> 1] * (e & 1 ? f.y : f.x);
+                        }
                     }
                 } else {
 #pragma unroll

@@ -110,14 +110,14 @@ struct BlockPages {
             }
         }
     }
-    // INT4: scales of page s: s_RK or s_RV of a head dimension, s_LV of a token.
-    __device__ __forceinline__ float dim_scale(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int kv, int dim) const {
+    // INT4: scales of page s: s_RK or s_RV of head dimensions dim, dim + 1 (dim even), s_LV of tokens t, t + 1 (t even).
+    __device__ __forceinline__ float2 dim_scales(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int kv, int dim) const {
         const unsigned char *at = buf + s * bl.fetch_bytes + bl.scales + (kv ? y.q_off_sRV - y.q_off_sRK : 0);
-        return __half2float(reinterpret_cast<const __half *>(at)[q4_dscale_index(dim)]);
+        return __half22float2(*reinterpret_cast<const __half2 *>(at + 2 * q4_dscale_index(dim)));
     }
-    __device__ __forceinline__ float token_scale(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int t) const {
+    __device__ __forceinline__ float2 token_scales(const Layout &y, const BlockLayout &bl, const unsigned char *buf, int s, int t) const {
         const unsigned char *at = buf + s * bl.fetch_bytes + bl.scales + (y.q_off_sLV - y.q_off_sRK);
-        return __half2float(reinterpret_cast<const __half *>(at)[q4_scale_index(y.P, t)]);
+        return __half22float2(*reinterpret_cast<const __half2 *>(at + 2 * q4_scale_index(y.P, t)));
     }
 };
 
@@ -247,12 +247,17 @@ struct RowTile {
             const int g = lane >> 2, c = lane & 3;
             float row[2] = {1.f, 1.f};
             if (kv)
-                for (int r2 = 0; r2 < 2; ++r2) row[r2] = bp.token_scale(y, bl, fetched, s, t0 + g + 8 * r2);
+                for (int r2 = 0; r2 < 2; ++r2) {
+                    const int t = t0 + g + 8 * r2;
+                    const float2 f = bp.token_scales(y, bl, fetched, s, t & ~1);
+                    row[r2] = t & 1 ? f.y : f.x;
+                }
 #pragma unroll
-            for (int j = 0; j < KT; ++j)
+            for (int j = 0; j < KT; ++j) {
+                const float2 f = bp.dim_scales(y, bl, fetched, s, kv, 8 * nt(j) + 2 * c);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[j][e] *= row[e >> 1] * bp.dim_scale(y, bl, fetched, s, kv, 8 * nt(j) + 2 * c + (e & 1));
+                for (int e = 0; e < 4; ++e) acc[j][e] *= row[e >> 1] * (e & 1 ? f.y : f.x);
+            }
         }
     }
     // Turn keys stored before RoPE by their positions pg P + t0 + row (the page
