@@ -145,7 +145,8 @@ __device__ __forceinline__ float finite_abs(float x) {
 // an item is short and waits on the one before, so CTAs stay and loop over
 // items: the next item's factors arrive and the last image leaves while one is
 // computed.  32K tokens x 8 heads, ranks 16 and 24: 51 us (3.9 TB/s; 82 us with a
-// CTA per block and 8 warps); INT4 records, whose codes are expanded first: 150 us.
+// CTA per block and 8 warps); INT4 records, whose codes are expanded first, take
+// about 95 us, keys before RoPE, turned here, 68.
 struct StageItem {
     int i, b, T0, T1, fw, h, blk, kv;
     StageItem() = default;
