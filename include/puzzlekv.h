@@ -384,9 +384,9 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t la
  *   q:       device, [N][num_q_heads][head_dim] in kv_dtype, N = sum of counts,
  *            the sequences' tokens one after another in list order;
  *   k, v:    device, [N][num_kv_heads][head_dim] in kv_dtype (keys before RoPE
- *            in stores with rope_theta > 0; queries already rotated).  Values
- *            of a chunk must be finite: an infinity or NaN in the v row of a
- *            token may reach the outputs of the chunk's earlier tokens.
+ *            in stores with rope_theta > 0; queries already rotated).  An
+ *            infinity or NaN in a token's row reaches the outputs of the tokens
+ *            that see it (a value's, its column alone), and no others.
  *   out:     device, [N][num_q_heads][head_dim] in kv_dtype.
  *   seq_ids, counts: host, B distinct slots, empty ones included, and the
  *            number of new tokens of each, 0 or more; at most

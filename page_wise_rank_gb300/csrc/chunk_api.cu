@@ -396,6 +396,7 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
             pl.g.scales = reinterpret_cast<float2 *>(w + pl.scales);
             pl.g.status = status_ptr(s);
             pl.f.q = static_cast<const char *>(q);
+            pl.f.v_new = pl.g.v_new;
             pl.f.out = static_cast<char *>(out);
             pl.f.images = pl.g.images;
             pl.f.scales = pl.g.scales;

@@ -202,11 +202,10 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
         const StageItem it = its[buf];
         const BlockPages bp(y, NP, it.blk * NP, it.fw, it.kv);
         unsigned char *pages = Q4 ? buffer(2) : buffer(buf);
-        if (bp.lo > 0 || bp.hi < NP) {
-            fetch_dense<P, D>(y, bp, p.dense_pool, it.kv ? p.v_new : p.k_new, p.off[it.i], p.layer, it.b, it.h, it.kv, it.T0,
-                              it.T1, pages, bl.page_bytes);
-            __syncthreads();
-        }
+        int bad = 0;
+        if (bp.lo > 0 || bp.hi < NP)
+            bad = __syncthreads_or(fetch_dense<P, D>(y, bp, p.dense_pool, it.kv ? p.v_new : p.k_new, p.off[it.i], p.layer, it.b,
+                                                     it.h, it.kv, it.T0, it.T1, pages, bl.page_bytes));
         if (bp.lo < bp.hi) {
             const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
             if (!ok) {  // let the copies land, then leave the images as they are
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                          "r"(smem_u32(img)), "r"((uint32_t)IMG)
                          : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            reinterpret_cast<float *>(p.scales)[item] = (float)scale;
+            reinterpret_cast<float *>(p.scales)[item] = (float)scale + (!bad ? 0.f : scale < 0 ? -0.25f : 0.25f);
         }
     }
     if (tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the images are written
@@ -724,6 +723,34 @@ __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
     }
 }
 
+// Block (entry, head), a thread to a column: infinities and NaN among the chunk's
+// values, left out of the images, into the outputs that see them: the weights
+// are positive, so each takes over its column from its token on.  Nearly always
+// nothing: the blocks' marks are read and that is all (2 to 8 us of a call; a
+// function called by the attention kernel took 4 % of its time, reached or not).
+template <int D>
+__global__ void __launch_bounds__(D) nonfinite_kernel(const FlashParams p) {
+    grid_dependency_wait();
+    const int i = blockIdx.x, h = blockIdx.y, c = threadIdx.x, nblk = p.blk_off[i + 1] - p.blk_off[i];
+    const float2 *scales = p.scales + (size_t)p.blk_off[i] * p.H + (size_t)h * nblk;
+    int bad = 0;
+    for (int blk = p.T[i] / FLASH_KEYS + c; blk < nblk; blk += D) bad |= scales[blk].y != truncf(scales[blk].y);
+    if (!__syncthreads_or(bad)) return;
+    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v_new) + ((size_t)p.off[i] * p.H + h) * D + c;
+    __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(p.out) + ((size_t)p.off[i] * p.Hq + h * p.G) * D + c;
+    float seen = 0.f;  // the sum of those up to token t
+#pragma unroll 8
+    for (int t = 0; t < p.n[i]; ++t) {
+        const float x = __bfloat162float(v[(size_t)t * p.H * D]);
+        if (!isfinite(x)) seen += x;
+        if (seen != 0.f)
+            for (int g = 0; g < p.G; ++g) {
+                __nv_bfloat16 &o = out[((size_t)t * p.Hq + g) * D];
+                o = __float2bfloat16_rn(__bfloat162float(o) + seen);
+            }
+    }
+}
+
 template <int P, int D, bool Q4>
 static cudaError_t stage_t(const StageParams &p, int num_sms, cudaStream_t st) {
     const int smem = FLASH_KEYS * D * 2 + (int)BlockLayout(p.y).smem(p.y, FLASH_KEYS / P);  // at most 32 + 2 x 41 KB
@@ -753,10 +780,13 @@ static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
     cudaError_t e = allow_smem<flash_kernel<D>>(smem);
     if (e != cudaSuccess) return e;
     e = launch_dependent(flash_kernel<D>, dim3((unsigned)p.ctas), FLASH_THREADS, smem, st, p);
-    if (e != cudaSuccess || p.ctas == 1) return e;
-    int most = 0;
-    for (int i = 0; i < p.nseq; ++i) most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
-    return launch_dependent(flash_merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st, p);
+    if (e == cudaSuccess && p.ctas > 1) {
+        int most = 0;
+        for (int i = 0; i < p.nseq; ++i) most = std::max(most, std::min(FLASH_ROWS, p.n[i] * p.G));
+        e = launch_dependent(flash_merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st, p);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_dependent(nonfinite_kernel<D>, dim3((unsigned)p.nseq, (unsigned)p.H), D, 0, st, p);
 }
 
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st) {

@@ -33,6 +33,7 @@ constexpr int SMALL_SLOTS = 16;
 struct SmallShared {
     uint64_t full[SMALL_SLOTS], empty[SMALL_SLOTS];
     int failed;
+    int bad;  // the chunk's values hold infinities or NaN
 };
 
 __device__ __forceinline__ float ex2s(float x) {
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
             mbar_init(&sh.full[k], 1);
             mbar_init(&sh.empty[k], RT);
         }
-        sh.failed = 0;
+        sh.failed = sh.bad = 0;
         fence_barrier_init();
     }
     grid_dependency_wait();  // the launch before may still write pages or queries
@@ -378,7 +379,9 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
     int issued = 0;
     if (leader)
         for (; issued < SPG; ++issued) issue(issued);
-    // the chunk's rows, swizzled, zeros past the last: units of UR rows
+    // the chunk's rows, swizzled, zeros past the last: units of UR rows; infinities
+    // and NaN among the values wait until the end, since earlier tokens weigh
+    // them by zero, which they would turn into NaN
     unsigned char *chunk = sm + (size_t)p.slots * p.unit_bytes;
     const int cu = sp == ns - 1 ? (n + UR - 1) / UR : 0;
     constexpr int CH = D / 8, AHEAD = 8;  // 16-byte chunks of a row; loads in flight
@@ -393,6 +396,11 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int e = e0 + a * 32 * SMALL_WARPS, ch = e % CH, kv = e / CH % 2, t = e / (2 * CH);
+            if (kv) {
+                int bad = 0;
+                v[a] = make_uint4(finite_pair(v[a].x, bad), finite_pair(v[a].y, bad), finite_pair(v[a].z, bad), finite_pair(v[a].w, bad));
+                if (bad) sh.bad = 1;
+            }
             if (t < cu * UR)
                 *reinterpret_cast<uint4 *>(chunk + (size_t)(t / UR) * 2 * HALF + kv * HALF + swz_offset(t % UR, 16 * ch, D * 2)) = v[a];
         }
@@ -484,6 +492,17 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
             o.z = fmaf(f, v.z, o.z);
             o.w = fmaf(f, v.w, o.w);
         }
+        if (sh.bad)  // those that the row sees, each into its column (the weights are positive)
+            for (int t = 0; t <= r / G; ++t) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(p.v_new + (((size_t)(p.off[i] + t) * y.H + h) * D + 4 * j) * 2);
+                int bad = 0;
+                const uint2 z = make_uint2(finite_pair(x.x, bad), finite_pair(x.y, bad));
+                if (!bad) continue;
+                if ((x.x ^ z.x) & 0xFFFFu) o.x += bf16_lo_to_f32(x.x);
+                if ((x.x ^ z.x) >> 16) o.y += bf16_hi_to_f32(x.x);
+                if ((x.y ^ z.y) & 0xFFFFu) o.z += bf16_lo_to_f32(x.y);
+                if ((x.y ^ z.y) >> 16) o.w += bf16_hi_to_f32(x.y);
+            }
         if (ns == 1) {
             const float il = 1.f / L;
             *reinterpret_cast<uint2 *>(p.out + ((((size_t)(p.off[i] + r / G) * y.Hq + h * G + r % G) * D) + 4 * j) * 2) =

@@ -245,6 +245,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// A bf16 pair with infinities and NaN replaced by zeros; sets `bad` if there were any.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t w, int &bad) {
+    const uint32_t keep = ((w & 0x7F80u) == 0x7F80u ? 0u : 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : 0xFFFF0000u);
+    bad |= keep != 0xFFFFFFFFu;
+    return w & keep;
+}
+
 // Pack two floats into bf16x2 (round to nearest even); `lo` goes to the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);

@@ -199,7 +199,9 @@ constexpr int FLASH_ROWS = 256, FLASH_KEYS = 128;  // query rows of a pair of ti
 // (keys [128][d], values transposed [d][128], both K-major in the 128-byte
 // swizzle) per KV head and block of 128 positions: entry i, head h, block b at
 // index (blk_off[i] H + h nblk(i) + b), nblk(i) = ceil((T[i] + n[i]) / 128).
-// scales holds each block's powers of two (key, value): row = image 2^scale.
+// scales holds each block's powers of two (key, value): row = image 2^scale.  A
+// value block whose chunk rows held infinities or NaN (zeros in the image) has a
+// quarter added to the magnitude of its power.
 struct StageParams {
     Layout y;
     const char *factor_pool, *dense_pool;
@@ -223,6 +225,7 @@ struct FlashParams {
     int H, Hq, G, nseq, ctas;
     float scale_log2;
     const char *q;
+    const char *v_new;
     char *out;
     const char *images;
     const float2 *scales;

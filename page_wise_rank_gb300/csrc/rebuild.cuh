@@ -123,9 +123,11 @@ struct BlockPages {
 
 // The other rows of the block into the buffer: position pos < T0 from the dense
 // pool, pos < T1 from row `row0 + pos - T0` of a chunk ([rows][H][D]), zeros past.
+// Infinities and NaN in a chunk's values become zeros: earlier tokens weigh them
+// by zero, which they would turn into NaN.  Returns whether the thread met any.
 // All threads; a barrier follows.
 template <int P, int D>
-__device__ __forceinline__ void fetch_dense(const Layout &y, const BlockPages &bp, const char *dense_pool, const char *chunk,
+__device__ __forceinline__ int fetch_dense(const Layout &y, const BlockPages &bp, const char *dense_pool, const char *chunk,
                                             int row0, int layer, int b, int h, int kv, int T0, int T1, unsigned char *buf,
                                             uint32_t page_bytes) {
     constexpr int CH = D / 8;  // 16-byte chunks of a row
@@ -141,12 +143,16 @@ __device__ __forceinline__ void fetch_dense(const Layout &y, const BlockPages &b
                                           swz_offset(row % P, 16 * ch, D * 2);
         v[k] = *reinterpret_cast<const uint4 *>(src);
     }
+    int bad = 0;
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         const int e = threadIdx.x + k * STAGE_THREADS, row = e / CH, ch = e % CH, s = row / P;
         if (s >= bp.lo && s < bp.hi) continue;
+        if (kv && bp.pg0 * P + row >= T0)
+            v[k] = make_uint4(finite_pair(v[k].x, bad), finite_pair(v[k].y, bad), finite_pair(v[k].z, bad), finite_pair(v[k].w, bad));
         *reinterpret_cast<uint4 *>(buf + s * page_bytes + swz_offset(row % P, 16 * ch, D * 2)) = v[k];
     }
+    return bad;
 }
 
 // Two accumulator registers pairs from bf16 pairs: of row g, and of row g + 8.

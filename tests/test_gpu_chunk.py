@@ -151,6 +151,49 @@ def test_sharp_and_flat_scores(pkv):
         assert excess(got[keep], ref[keep], bound[keep]) <= 1.0
 
 
+@pytest.mark.parametrize("name", ["llama", "g3-d64", "g1-p16", "int4", "prerope", "fp32", "p64-d64"])
+@pytest.mark.parametrize("T,n", [(0, 2), (5, 9), (1537, 6), (1537, 200), (130, 300)])
+def test_nonfinite_tokens_reach_no_earlier_token(pkv, name, T, n):
+    """Infinities and NaN in a value row turn their columns of the outputs that see them (weights are positive), and
+    NaN in a key row the outputs of its own token; every other element is as if they were not there."""
+    cfg = make_cfg(pkv, **STORES[name])
+    store, host = filled(pkv, cfg, [T, 77, 0, 0])
+    k, v = random_rows(cfg, n + 3, 31)
+    q = queries(cfg, n + 3, 32)
+    at, inf = n // 2, float("inf")
+    poison = {0: inf, 9: float("nan"), cfg.head_dim - 1: -inf}
+    bad_k, bad_v = k.clone(), v.clone()
+    for c, x in poison.items():
+        bad_v[at, 0, c], v[at, 0, c] = x, 0.0
+    bad_k[n - 1, :, 5] = float("nan")
+    out = store.chunk_attention(0, q.cuda(), bad_k.cuda(), bad_v.cuda(), [0, 1], [n, 3]).double().cpu().numpy()
+    last, out[n - 1] = out[n - 1].copy(), 0.0
+    assert np.isnan(last).all()
+    G = cfg.num_q_heads // cfg.num_kv_heads
+    for c, x in poison.items():
+        got = out[at:n - 1, :G, c]
+        assert np.isnan(got).all() if np.isnan(x) else (got == x).all()
+        out[at:n - 1, :G, c] = 0.0
+    ref, bound = chunk_reference(cfg, cache_rows(store, cfg, host, 0, 0, T), k[:n], v[:n], q[:n], T)
+    ref[n - 1] = 0.0
+    ref[at:n - 1, :G, list(poison)] = 0.0
+    assert excess(out[:n], ref, bound) <= 1.0
+    ref, bound = chunk_reference(cfg, cache_rows(store, cfg, host, 1, 0, 77), k[n:], v[n:], q[n:], 77)
+    assert excess(out[n:], ref, bound) <= 1.0
+    assert store.check_device_status() == 0
+
+
+@pytest.mark.parametrize("n", [20, 1500])
+def test_all_values_nonfinite(pkv, n):
+    """Every value of a long chunk NaN: the answers are NaN, and the call ends as soon as any other."""
+    cfg = make_cfg(pkv, num_layers=1, max_tokens_per_seq=4096)
+    store, _ = filled(pkv, cfg, [400, 0, 0, 0])
+    k, v = random_rows(cfg, n, 31)
+    out = store.chunk_attention(0, queries(cfg, n, 2).cuda(), k.cuda(), torch.full_like(v, float("nan")).cuda(), [0], [n])
+    assert out.isnan().all()
+    assert store.check_device_status() == 0
+
+
 def test_rows_beyond_the_lists_are_left_alone(pkv):
     """Padding after the last sequence (NaN inputs, a marked output) is neither read nor written."""
     cfg = make_cfg(pkv)
