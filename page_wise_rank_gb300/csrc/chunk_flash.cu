@@ -723,13 +723,22 @@ __global__ void __launch_bounds__(256) flash_merge_kernel(const FlashParams p) {
     }
 }
 
+// What nonfinite_kernel needs of FlashParams, whose 9 KB make a launch 3 us longer.
+struct NonfiniteParams {
+    int H, Hq, G;
+    const char *v_new;
+    char *out;
+    const float2 *scales;
+    int T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH], blk_off[MAX_CALL_BATCH + 1];
+};
+
 // Block (entry, head), a thread to a column: infinities and NaN among the chunk's
 // values, left out of the images, into the outputs that see them: the weights
 // are positive, so each takes over its column from its token on.  Nearly always
 // nothing: the blocks' marks are read and that is all (2 to 8 us of a call; a
 // function called by the attention kernel took 4 % of its time, reached or not).
 template <int D>
-__global__ void __launch_bounds__(D) nonfinite_kernel(const FlashParams p) {
+__global__ void __launch_bounds__(D) nonfinite_kernel(const NonfiniteParams p) {
     grid_dependency_wait();
     const int i = blockIdx.x, h = blockIdx.y, c = threadIdx.x, nblk = p.blk_off[i + 1] - p.blk_off[i];
     const float2 *scales = p.scales + (size_t)p.blk_off[i] * p.H + (size_t)h * nblk;
@@ -786,7 +795,16 @@ static cudaError_t flash_t(const FlashParams &p, cudaStream_t st) {
         e = launch_dependent(flash_merge_kernel<D>, dim3((unsigned)(p.ctas - 1), (unsigned)((most + 7) / 8)), 256, 0, st, p);
     }
     if (e != cudaSuccess) return e;
-    return launch_dependent(nonfinite_kernel<D>, dim3((unsigned)p.nseq, (unsigned)p.H), D, 0, st, p);
+    NonfiniteParams np;
+    np.H = p.H; np.Hq = p.Hq; np.G = p.G;
+    np.v_new = p.v_new;
+    np.out = p.out;
+    np.scales = p.scales;
+    for (int i = 0; i <= p.nseq; ++i) np.blk_off[i] = p.blk_off[i];
+    for (int i = 0; i < p.nseq; ++i) {
+        np.T[i] = p.T[i]; np.n[i] = p.n[i]; np.off[i] = p.off[i];
+    }
+    return launch_dependent(nonfinite_kernel<D>, dim3((unsigned)p.nseq, (unsigned)p.H), D, 0, st, np);
 }
 
 cudaError_t launch_flash(const FlashParams &p, int d, cudaStream_t st) {
