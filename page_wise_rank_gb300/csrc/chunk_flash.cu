@@ -121,6 +121,16 @@ __device__ __forceinline__ int fp16_exponent(float m) {
     const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127 - 12;
     return max(-110, min(e, 115));
 }
+// The power of a value block: a multiple of four, so that the blocks of a
+// sequence mostly share it, with the largest finite |x| = m in [2^11, 2^15): 11
+// bits down to 2^-25 of m or less, whatever the size of the values.  A block of
+// zeros has none.
+constexpr int NO_VALUES = -120;
+__device__ __forceinline__ int value_exponent(float m) {
+    if (!(m > 0.f)) return NO_VALUES;
+    const int e = (int)((__float_as_uint(m) >> 23) & 255) - 127 - 11;
+    return max(-108, e & ~3);
+}
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 __device__ __forceinline__ float finite_abs(float x) {
     const float a = fabsf(x);
@@ -317,9 +327,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
                     }
                 }
             }
-            // values of ordinary size keep scale 1, so that a sequence's blocks agree
-            const float vmax = block_max(KR / 8);
-            scale = vmax > 0.f && (vmax >= 32768.f || vmax < 0.00390625f) ? fp16_exponent(vmax) : 0;
+            scale = value_exponent(block_max(KR / 8));
             const float f = pow2i(-scale);
 #pragma unroll
             for (int j = 0; j < KR / 8; ++j)
@@ -436,7 +444,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
             tc_fence_before();  // the previous piece's O has been read
             mbar_arrive(&s.q_full[t]);
             float m = -INFINITY, l = 0.f;
-            int E = 0;
+            int E = 0, top = 0;  // O is in units of 2^E; the largest E so far
             const float2 *scales = p.scales + pc.image(0);
             float2 sc = scales[pc.cb0];
             const int full = (p.T[i] + r0 / G + 1) / FLASH_KEYS;  // blocks before it are seen whole by every row of the tile
@@ -479,21 +487,24 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 mx *= cf;
                 // The reference m moves only when a score exceeds it by 2^8 (the
                 // weights then stay below 2^8, far inside fp16), so O is rescaled
-                // rarely; a value block of a larger scale rescales it as well.
+                // rarely.  A value block whose power is above E, or two steps below,
+                // rescales it as well, exactly: a block's weights are never
+                // more than one step short of their bits.  (A power 2^60 below
+                // the largest stays short: O, at most 2^23 T units, must not overflow.)
                 float f = 1.f;
                 if (blk == pc.cb0) {
                     m = mx;
-                    E = ev;
+                    E = top = ev;
                 } else {
                     if (mx > m + 8.f) {
                         f = m == -INFINITY ? 1.f : ex2(m - mx);
                         m = mx;
                         l *= f;
                     }
-                    if (ev > E) {
-                        f *= pow2i(max(E - ev, -126));
-                        E = ev;
-                    }
+                    const int to = ev > E ? ev : ev < E - 4 && ev != NO_VALUES ? max(ev, min(E, top - 60)) : E;
+                    f *= pow2i(max(E - to, -126));
+                    E = to;
+                    top = max(top, E);
                     if (__any_sync(0xffffffffu, f != 1.f)) {
                         for (int k = 0; k < D / 32; ++k) {
                             uint32_t o[32];
@@ -505,7 +516,8 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                         }
                     }
                 }
-                const float up = (float)max(ev - E, -120);  // 2^up: this block's values in units of O
+                // 2^up: this block's values in units of O (2^-41 of a weight is zero in fp16)
+                const float up = ev == NO_VALUES ? 0.f : (float)max(ev - E, -41);
                 const float off = (m == -INFINITY ? 0.f : m) - up;
                 uint64_t sum[2] = {0, 0};  // pairs of zeros
                 const uint64_t cf2 = pair(cf, cf), off2 = pair(-off, -off);
