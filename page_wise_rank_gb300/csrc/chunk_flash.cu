@@ -485,12 +485,13 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                     mx = fmaxf(max3(max3(a[0], a[1], a[2]), a[3], a[4]), max3(a[5], a[6], a[7]));
                 }
                 mx *= cf;
-                // The reference m moves only when a score exceeds it by 2^8 (the
-                // weights then stay below 2^8, far inside fp16), so O is rescaled
-                // rarely.  A value block whose power is above E, or two steps below,
+                // The reference m moves only when a score exceeds it by 2^8, so O is
+                // rescaled rarely.  The weights are 2^7 times 2^(s - m), up to 2^15: fp16
+                // holds them in full down to 2^-21 of the reference's and to a step
+                // of 2^-31 below, so that a long tail still counts.  A value block whose power is above E, or two steps below,
                 // rescales it as well, exactly: a block's weights are never
                 // more than one step short of their bits.  (A power 2^60 below
-                // the largest stays short: O, at most 2^23 T units, must not overflow.)
+                // the largest stays short: O, at most 2^30 T units, must not overflow.)
                 float f = 1.f;
                 if (blk == pc.cb0) {
                     m = mx;
@@ -516,9 +517,9 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                         }
                     }
                 }
-                // 2^up: this block's values in units of O (2^-41 of a weight is zero in fp16)
+                // 2^up: this block's values in units of O (2^-41 of any weight is zero in fp16)
                 const float up = ev == NO_VALUES ? 0.f : (float)max(ev - E, -41);
-                const float off = (m == -INFINITY ? 0.f : m) - up;
+                const float off = (m == -INFINITY ? 0.f : m) - up - 7.f;
                 uint64_t sum[2] = {0, 0};  // pairs of zeros
                 const uint64_t cf2 = pair(cf, cf), off2 = pair(-off, -off);
 #pragma unroll

@@ -114,3 +114,31 @@ def test_values_of_unlike_sizes(pkv, kind, name):
     few = store.chunk_attention(0, q[:5].cuda(), kn[:5].cuda(), vn[:5].cuda(), [0], [5])
     assert excess_of_tokens(cfg, rows, kn, vn, q, T, range(5), few) <= 1.0
     assert store.check_device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [20.5, 25.5, 28.0])
+def test_long_tails_count(pkv, bits):
+    """One key draws nearly all weight and its value is zero: the answer is what thousands of keys of 2^-bits of its
+    weight add up to.  All blocks share a power here, and weights are held to 2^-32 of the largest."""
+    T, n = 3600, 1024
+    cfg = make_cfg(pkv, num_layers=1, num_kv_heads=8, num_q_heads=32, max_batch=1, max_tokens_per_seq=T + n,
+                   recent_tokens=T)
+    H, d = cfg.num_kv_heads, cfg.head_dim
+    g = torch.Generator().manual_seed(5)
+    axis = torch.zeros(d)
+    axis[3] = 1.0
+    k = 0.05 * torch.randn(H, T + n, d, generator=g)
+    k[:, 0] = axis * (bits * math.log(2) * math.sqrt(d) / 8)
+    v = 1 + 0.1 * torch.randn(H, T + n, d, generator=g)
+    v[:, 0] = 0.0
+    q = (8 * axis).expand(n, cfg.num_q_heads, d)
+    k, v, q = k.to(cfg.kv_dtype), v.to(cfg.kv_dtype), q.to(cfg.kv_dtype).contiguous()
+    store, host = pkv.Store(cfg), HostCache()
+    store.load_prefill(0, k[None, :, :T].contiguous().cuda(), v[None, :, :T].contiguous().cuda())
+    host.set_prefill(0, k[None, :, :T], v[None, :, :T])
+    kn, vn = (x[:, T:].transpose(0, 1).contiguous() for x in (k, v))
+    out = store.chunk_attention(0, q.cuda(), kn.cuda(), vn.cuda(), [0], [n])
+    rows = cache_rows(store, cfg, host, 0, 0, T)
+    assert excess_of_tokens(cfg, rows, kn, vn, q, T, range(0, n, 100), out, 2.0 ** -32) <= 1.0
+    few = store.chunk_attention(0, q[:5].cuda(), kn[:5].cuda(), vn[:5].cuda(), [0], [5])
+    assert excess_of_tokens(cfg, rows, kn, vn, q, T, range(5), few, 2.0 ** -32) <= 1.0
