@@ -5,6 +5,7 @@
 // K^T into tensor memory, the online softmax in registers (one row per
 // thread), P back into tensor memory as the next product's operand, O += P V.
 #include <algorithm>
+#include <cfloat>
 
 #include "kernels.h"
 #include "rebuild.cuh"
@@ -450,7 +451,9 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
             const int full = (p.T[i] + r0 / G + 1) / FLASH_KEYS;  // blocks before it are seen whole by every row of the tile
             bool ok = true;
             for (int blk = pc.cb0; blk < pc.cb1; ++blk) {
-                const float cf = qs * pow2i((int)sc.x);
+                // a positive normal number whatever the operands' sizes: masked scores
+                // are minus infinity and others may be zero, times this factor
+                const float cf = fminf(fmaxf(qs * pow2i((int)sc.x), FLT_MIN), FLT_MAX);
                 const int ev = (int)sc.y;
                 if (blk + 1 < pc.cb1) sc = scales[blk + 1];
                 // a warp leaves as one: tensor-memory accesses are whole-warp operations

@@ -142,3 +142,37 @@ def test_long_tails_count(pkv, bits):
     assert excess_of_tokens(cfg, rows, kn, vn, q, T, range(0, n, 100), out, 2.0 ** -32) <= 1.0
     few = store.chunk_attention(0, q[:5].cuda(), kn[:5].cuda(), vn[:5].cuda(), [0], [5])
     assert excess_of_tokens(cfg, rows, kn, vn, q, T, range(5), few, 2.0 ** -32) <= 1.0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int4", "prerope", "d64-p16"])
+@pytest.mark.parametrize("power", [-66, -60, -120, 120])
+def test_products_outside_fp32(pkv, kind, power):
+    """Queries and keys of 2^power: products at fp32's lower end or under it and, at 2^120, zeros beside factors whose
+    product overflows.  All scores are zero, or as good as: every answer is the mean of the seen values."""
+    cfg = make_cfg(pkv, num_layers=1, max_batch=2, **{**KINDS[kind], "recent_tokens": 128})  # nothing is factorized
+    T, n, H, d = 100, 150, cfg.num_kv_heads, cfg.head_dim
+    g = torch.Generator().manual_seed(power + 200)
+    size = 2.0 ** power
+    k, v = (torch.randn(H, T + n, d, generator=g) for _ in range(2))
+    q = torch.randn(n, cfg.num_q_heads, d, generator=g)
+    if power > 0:  # orthogonal supports (pairs that RoPE turns stay inside one of them)
+        odd = (torch.arange(d) % (d // 2)) % 2 == 1
+        k, q = torch.where(odd, k.sign(), 0.0), torch.where(odd, 0.0, q.sign())
+    k, q, v = (k * size).to(cfg.kv_dtype), (q * size).to(cfg.kv_dtype), v.to(cfg.kv_dtype)
+    store = pkv.Store(cfg)
+    store.append_chunk(0, *(x[:, :T].transpose(0, 1).contiguous().cuda() for x in (k, v)), [0], [T])
+    kn, vn = (x[:, T:].transpose(0, 1).contiguous() for x in (k, v))
+    V = v.double().numpy()
+    G = cfg.num_q_heads // H
+    for m in (n, 5):
+        out = store.chunk_attention(0, q[:m].cuda(), kn[:m].cuda(), vn[:m].cuda(), [0], [m]).double().cpu().numpy()
+        assert np.isfinite(out).all()
+        for j in range(m):
+            for h in range(H):
+                seen = V[h, :T + j + 1]
+                # weights and values are off by 2^-11 each and by 2^-36 of the largest value;
+                # scores are below 2^-80
+                inner = 2.05 * 2.0 ** -11 * np.abs(seen).mean(0) + 2.0 ** -30 * np.abs(V).max()
+                bound = inner + 2.0 ** -8 * (np.abs(seen.mean(0)) + inner)
+                assert (np.abs(out[j, h * G:(h + 1) * G] - seen.mean(0)) <= bound).all()
+    assert store.check_device_status() == 0
