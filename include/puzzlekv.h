@@ -182,7 +182,7 @@ puzzlekv_status puzzlekv_factorize_pages(puzzlekv_store *store, const int32_t *s
  * factorization also runs on `stream`.  With async = 1 it runs on the
  * store's internal low-priority stream, after the work already queued on
  * `stream`, so that the caller's next layers (their dense attention) overlap
- * it; the sequence's next attention call waits for it.
+ * it; attention calls on the sequence wait for it, each stream for itself.
  *   k, v: device, [num_kv_heads][T][head_dim] in kv_dtype.  With async = 0
  *         they may be freed once the stream passes this call; with async = 1
  *         they are read on the internal stream (puzzlekv_background_stream),
@@ -303,14 +303,14 @@ puzzlekv_status puzzlekv_decode_attention(puzzlekv_store *store, int32_t layer, 
  *   after everything already queued on `stream`, one CTA per page job, so
  *   that it overlaps the decode steps that follow instead of stalling them.
  *   A batch's factors are first read when one of its pages becomes
- *   factorized; the first decode call (puzzlekv_decode_attention,
- *   puzzlekv_decode_step, the static-scratch variant) that reaches that
- *   length, and any prefill call (puzzlekv_load_prefill,
- *   puzzlekv_factorize_layer) that rewrites one of the batch's layers, makes
- *   its own stream wait for the batch.  puzzlekv_check_device_status and
- *   puzzlekv_factorize_counters synchronise the internal stream as well; the
- *   store must not be destroyed while its caller's streams still hold work
- *   that waits on a batch.
+ *   factorized; every call that attends, reads or appends a chunk at or past
+ *   that length (puzzlekv_append_token alone does not read the page), and any
+ *   prefill call (puzzlekv_load_prefill, puzzlekv_factorize_layer) that
+ *   rewrites one of the batch's layers, makes its own stream wait for the
+ *   batch until that has finished, whichever streams have waited before.
+ *   puzzlekv_check_device_status and puzzlekv_factorize_counters synchronise
+ *   the internal stream as well; the store must not be destroyed while its
+ *   caller's streams still hold work that waits on a batch.
  */
 puzzlekv_status puzzlekv_convert_ready_pages(puzzlekv_store *store, void *stream);
 
@@ -394,7 +394,8 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t la
  *   work:    device, 256-byte aligned, work_bytes >= what
  *            puzzlekv_chunk_workspace reports; its contents are scratch.
  * The call may be captured into a CUDA graph when no background work of the
- * store is pending (puzzlekv_wait_background before the capture;
+ * store is pending (puzzlekv_wait_background before the capture, on the
+ * captured stream unless that work has finished by then;
  * PUZZLEKV_ERR_UNSUPPORTED otherwise); a replay attends the store's content at
  * the lengths it was captured with.  Calls that may run at the same time, on
  * two streams or in two graphs, need workspaces of their own.  If a bounded wait

@@ -119,6 +119,36 @@ void layout_from(Layout &y, const puzzlekv_config *c) {
 
 constexpr int kConvBatches = 8;
 
+bool pkv::batch_finished(const puzzlekv_store::ConvBatch &cb) {
+    // a query is refused while a stream is captured, unless the thread says that it means it
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return false;
+    const cudaError_t e = cudaEventQuery(cb.done);
+    (void)cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) (void)cudaGetLastError();  // leave nothing behind for later launch checks
+    return e == cudaSuccess;
+}
+
+bool pkv::wait_batch(puzzlekv_store::ConvBatch &cb, cudaStream_t strm) {
+    if (batch_finished(cb)) {
+        cb.pending = false;
+        return false;
+    }
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(strm, &capture) == cudaSuccess && capture != cudaStreamCaptureStatusNone) {
+        if (!cb.waited.empty()) return false;  // a capture cannot wait for work outside it: who captures has waited before
+        cudaStreamWaitEvent(strm, cb.done, 0);
+        return true;
+    }
+    unsigned long long id = 0;
+    const bool known = cudaStreamGetId(strm, &id) == cudaSuccess;
+    if (known)
+        for (const auto &w : cb.waited)
+            if (w.id == id) return false;
+    if (cudaStreamWaitEvent(strm, cb.done, 0) == cudaSuccess && known) cb.waited.push_back({id, strm});
+    return true;
+}
+
 bool pkv::wait_conversions(puzzlekv_store *s, cudaStream_t strm, const int32_t *seq_ids, const int *lens, int B,
                            bool all) {
     bool waited = false;
@@ -126,20 +156,16 @@ bool pkv::wait_conversions(puzzlekv_store *s, cudaStream_t strm, const int32_t *
         if (!cb.pending) continue;
         bool due = all;
         for (int i = 0; i < B && !due; ++i) due = lens[i] >= cb.deadline[seq_ids[i]];
-        if (due) {
-            cudaStreamWaitEvent(strm, cb.done, 0);
-            cb.pending = false;
-            waited = true;
-        }
+        if (due && wait_batch(cb, strm)) waited = true;
     }
     return waited;
 }
 
 // Background batches run on the store's internal lowest-priority stream,
-// created on first use.  begin_batch takes the next ring entry (ordering the
-// caller's stream after the entry's previous batch if that is still
-// pending), clears its deadlines and orders the internal stream after the
-// work already queued on `strm`; end_batch marks the batch's end.
+// created on first use.  begin_batch takes the next ring entry and orders the
+// internal stream after the work already queued on `strm`; end_batch marks the
+// batch's end.  An entry whose previous batch still runs keeps that batch's
+// deadlines: the new event comes later in the same stream and covers both.
 static cudaError_t ensure_background(puzzlekv_store *s) {
     if (s->conv_stream) return cudaSuccess;
     int least = 0, greatest = 0;
@@ -160,12 +186,12 @@ static cudaError_t begin_batch(puzzlekv_store *s, cudaStream_t strm, puzzlekv_st
     if (e != cudaSuccess) return e;
     puzzlekv_store::ConvBatch &cb = s->batches[s->next_batch];
     s->next_batch = (s->next_batch + 1) % kConvBatches;
-    if (cb.pending) {  // its event is about to be reused: order the caller's stream after it now
-        e = cudaStreamWaitEvent(strm, cb.done, 0);
+    if (!cb.pending || batch_finished(cb)) {
         cb.pending = false;
+        std::fill(cb.deadline.begin(), cb.deadline.end(), INT_MAX);
+        std::fill(cb.uses.begin(), cb.uses.end(), 0);
     }
-    std::fill(cb.deadline.begin(), cb.deadline.end(), INT_MAX);
-    std::fill(cb.uses.begin(), cb.uses.end(), 0);
+    cb.waited.clear();
     // the batch reads what the caller's stream has written: start after it
     if (e == cudaSuccess) e = cudaEventRecord(s->conv_ready, strm);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(s->conv_stream, s->conv_ready, 0);
@@ -312,10 +338,7 @@ static puzzlekv_status prefill(puzzlekv_store *s, int32_t seq, int32_t layer0, i
     for (auto &cb : s->batches) {
         bool uses = false;
         for (int l = layer0; cb.pending && l < layer0 + n_layers && !uses; ++l) uses = cb.uses[(size_t)seq * y.L + l];
-        if (uses) {
-            cudaStreamWaitEvent(strm, cb.done, 0);
-            cb.pending = false;
-        }
+        if (uses) wait_batch(cb, strm);
     }
     cudaError_t e = launch_seq_init(ip, strm);
     s->after_decode = false;

@@ -45,7 +45,9 @@ puzzlekv_status refuse_capture(cudaStream_t strm) {
     return PUZZLEKV_OK;
 }
 
-// A captured call cannot wait for background work queued outside the capture.
+// A captured call cannot wait for background work queued outside the capture:
+// a batch must have been waited for, and by the captured stream unless it has
+// finished since.
 puzzlekv_status refuse_pending(const puzzlekv_store *s, cudaStream_t strm) {
     bool pending = false;
     for (const auto &cb : s->batches) pending |= cb.pending;
@@ -53,8 +55,14 @@ puzzlekv_status refuse_pending(const puzzlekv_store *s, cudaStream_t strm) {
     cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
     const cudaError_t e = cudaStreamIsCapturing(strm, &c);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
-    if (c != cudaStreamCaptureStatusNone)
-        return fail(PUZZLEKV_ERR_UNSUPPORTED, "background conversions are pending: call puzzlekv_wait_background before the capture");
+    if (c == cudaStreamCaptureStatusNone) return PUZZLEKV_OK;
+    for (const auto &cb : s->batches) {
+        if (!cb.pending) continue;
+        bool here = false;
+        for (const auto &w : cb.waited) here |= w.stream == strm;
+        if (!here && (cb.waited.empty() || !batch_finished(cb)))
+            return fail(PUZZLEKV_ERR_UNSUPPORTED, "background conversions are pending: call puzzlekv_wait_background before the capture");
+    }
     return PUZZLEKV_OK;
 }
 

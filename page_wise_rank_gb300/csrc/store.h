@@ -53,12 +53,19 @@ struct puzzlekv_store {
     int num_sms;
     // Batched conversions run on an internal low-priority stream.  A batch's
     // factor records are first read when one of its pages becomes
-    // factorized, i.e. when its sequence reaches deadline[seq] tokens; the
-    // first call that attends at or past that length makes the caller's
-    // stream wait for the batch.
+    // factorized, i.e. when its sequence reaches deadline[seq] tokens; every
+    // stream whose calls attend at or past that length waits for the batch,
+    // until it is known to have finished.
     struct ConvBatch {
         cudaEvent_t done = nullptr;
-        bool pending = false;
+        bool pending = false;       // queued, and not known to have finished
+        // The streams ordered after it.  Ids, unlike handles, are not used again
+        // for later streams, but a captured stream's cannot be asked for.
+        struct Waiter {
+            unsigned long long id;
+            cudaStream_t stream;
+        };
+        std::vector<Waiter> waited;
         std::vector<int> deadline;  // [seq]: length at which the batch's first page is factorized
         std::vector<char> uses;     // [seq][layer]: the batch writes factor records of that layer
     };
@@ -108,6 +115,11 @@ inline void grow_dense(puzzlekv_store *s, int b, int l, int T) {
     lo = std::max(lo, (T - 1) / s->y.P - s->y.ring + 1);
 }
 
+// Has the batch finished on the device?  (Also while some stream is captured.)
+bool batch_finished(const puzzlekv_store::ConvBatch &cb);
+// Make `strm` wait for a batch, unless it has finished or `strm` has waited
+// already.  Returns true if a wait was inserted.
+bool wait_batch(puzzlekv_store::ConvBatch &cb, cudaStream_t strm);
 // Make `strm` wait for every pending background conversion batch that the
 // listed sequences (at the given lengths) reach, or for all of them when
 // `all` is set.  Returns true if a wait was inserted.
