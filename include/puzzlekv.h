@@ -303,11 +303,11 @@ puzzlekv_status puzzlekv_decode_attention(puzzlekv_store *store, int32_t layer, 
  *   after everything already queued on `stream`, one CTA per page job, so
  *   that it overlaps the decode steps that follow instead of stalling them.
  *   A batch's factors are first read when one of its pages becomes
- *   factorized; every call that attends, reads or appends a chunk at or past
- *   that length (puzzlekv_append_token alone does not read the page), and any
- *   prefill call (puzzlekv_load_prefill, puzzlekv_factorize_layer) that
- *   rewrites one of the batch's layers, makes its own stream wait for the
- *   batch until that has finished, whichever streams have waited before.
+ *   factorized; every call that attends, reads or appends at or past that
+ *   length, and any prefill call (puzzlekv_load_prefill,
+ *   puzzlekv_factorize_layer) that rewrites one of the batch's layers, makes
+ *   its own stream wait for the batch until that has finished, whichever
+ *   streams have waited before.
  *   puzzlekv_check_device_status and puzzlekv_factorize_counters synchronise
  *   the internal stream as well; the store must not be destroyed while its
  *   caller's streams still hold work that waits on a batch.

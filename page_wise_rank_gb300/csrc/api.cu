@@ -573,9 +573,11 @@ puzzlekv_status puzzlekv_append_token(puzzlekv_store *s, int32_t layer, const vo
     ap.nseq = B;
     FactorParams fp{};
     fp.n_conv = 0;
+    int grown[MAX_CALL_BATCH];
     for (int i = 0; i < B; ++i) {
         const int T = s->len[(size_t)seq_ids[i] * y.L + layer];
         if (T + 1 > y.Tmax) return fail(PUZZLEKV_ERR_CAPACITY, "sequence %d is full (%d tokens)", seq_ids[i], T);
+        grown[i] = T + 1;
     }
     for (int i = 0; i < B; ++i) {
         int b = seq_ids[i];
@@ -592,6 +594,9 @@ puzzlekv_status puzzlekv_append_token(puzzlekv_store *s, int32_t layer, const vo
         }
     }
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    // a background batch still reads its pages' ring slots, which come round
+    // no sooner than a page past its deadline
+    wait_conversions(s, strm, seq_ids, grown, B);
     cudaError_t e = launch_append(ap, strm);
     s->after_decode = false;
     if (e != cudaSuccess) return cuda_fail(e, "append launch");

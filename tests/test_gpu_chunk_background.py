@@ -91,6 +91,27 @@ def test_conversions_beside_two_streams(pkv):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
+@pytest.mark.parametrize("name", ["llama", "nosink-nowindow"])
+def test_tokens_alone_after_a_conversion(pkv, name):
+    """Appends that never attend, past the ring's round: the batch's pages keep the rows it reads."""
+    cfg = make_cfg(pkv, **STORES[name])
+    want, got = pkv.Store(cfg), pkv.Store(cfg)
+    K, V = (x.cuda() for x in random_rows(cfg, 640, 20, cfg.num_layers))
+    n = 450
+    k, v = (x.cuda() for x in random_rows(cfg, n, 21))
+    for s in (want, got):
+        s.load_prefill(0, K, V)
+    for layer in range(cfg.num_layers):
+        want.append_chunk(layer, k, v, [0], [n])
+    for t in range(n):
+        for layer in range(cfg.num_layers):
+            got.append_token(layer, k[t:t + 1], v[t:t + 1], [0])
+        got.convert_ready_pages()
+    for layer in range(cfg.num_layers):
+        for x, y in zip(want.read_tokens(layer, [0], [0], [640 + n]), got.read_tokens(layer, [0], [0], [640 + n])):
+            assert torch.equal(x, y)
+
+
 def test_more_batches_than_events(pkv):
     """More layers in the background than the store keeps events for."""
     T, L = 400, 13
