@@ -6,9 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "layout.h"
+#include "smem_limit.h"
 
 namespace pkv {
 
@@ -141,19 +140,16 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 // launch it would cost more host time than a small launch takes on the GPU.
 template <auto Kernel>
 inline cudaError_t allow_smem(size_t bytes) {
-    static std::atomic<int> allowed[64];
+    static SmemLimit limit;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (allowed[dev].load(std::memory_order_acquire) >= (int)bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    int had = allowed[dev].load();
-    while (e == cudaSuccess && had < (int)bytes && !allowed[dev].compare_exchange_weak(had, (int)bytes)) {
-    }
-    return e;
+    if (dev < 0 || dev >= SmemLimit::kDevices) return cudaErrorInvalidDevice;
+    return static_cast<cudaError_t>(limit.raise(dev, (int)bytes, [](int n) -> int {
+        const cudaError_t s = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+        if (s != cudaSuccess) return s;
+        return cudaFuncSetAttribute(Kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    }));
 }
 
 // Launch a kernel that begins with grid_dependency_wait in every block: it may
