@@ -1264,13 +1264,12 @@ cudaError_t launch_bf16(DecodeParams &p, long total_pages, int max_pages, int nu
             c.stages = NS;
             c.smem = NS * stage_bytes + NS * sizeof(uint64_t) + sizeof(DecodeShared<Shape::DU>) +
                      (ROPE ? 16 + (size_t)P * D * 4 : 0);  // RoPE: the aligned in-page angle table
-            c.err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)c.smem);
-            // An SM's shared/L1 split is set when it takes a CTA and holds
-            // while any CTA runs there: with the largest split a background
-            // factorization CTA still fits beside a decode CTA.
-            if (c.err == cudaSuccess)
-                c.err = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
+            // The limit is the kernel's, whatever the record size: it is only
+            // ever raised.  An SM's shared/L1 split is set when it takes a CTA
+            // and holds while any CTA runs there: with the largest split (set
+            // there too) a background factorization CTA still fits beside a
+            // decode CTA.
+            c.err = allow_smem<decode_bf16_kernel<P, D, RKT, RVT, Q4, ROPE>>(c.smem);
             if (c.err == cudaSuccess &&
                 (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&c.occ, k, Shape::NWC * 32, c.smem) != cudaSuccess ||
                  c.occ < 1))
