@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
         s.failed = 0;
         fence_barrier_init();
     }
+    __syncwarp();  // the allocation is the whole warp's
     if (warp == 0) tmem_alloc(&s.tmem, 512);
     tc_fence_before();
     __syncthreads();
@@ -563,6 +564,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
+                __syncwarp();  // the read is the whole warp's, the stores are the live rows'
                 tmem_ld32(tO + 32 * k, o);
                 tc_wait_ld();
                 if (live && whole) {
@@ -580,7 +582,6 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                             make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
                                         __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
                 }
-                __syncwarp();  // the next read is the whole warp's
             }
         }
     } else {

@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
             if (!ok) break;
             // the slot of the unit before is free, or nearly: the next copy goes there
             if (leader && k > 0 && (ok = issue(issued))) ++issued;
+            __syncwarp();  // the products below are the whole warp's
             int page, row;
             unit(pg + k * PG, page, row);
             const uint32_t at = smem_u32(sm + (size_t)sl * p.unit_bytes);
