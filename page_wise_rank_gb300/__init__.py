@@ -48,7 +48,7 @@ class StoreConfig:
             elif ctype is ctypes.c_float:
                 setattr(c, name, float(getattr(self, name)))
             else:
-                setattr(c, name, int(getattr(self, name)))
+                setattr(c, name, _lib.Int32.from_param(int(getattr(self, name))).value)
         return c
 
 
@@ -77,14 +77,17 @@ def _seq_ids(seq_ids: Sequence[int]):
     if arr is None:
         if len(_SEQ_CACHE) > 4096:
             _SEQ_CACHE.clear()
-        arr = _SEQ_CACHE[key] = (ctypes.c_int32 * len(key))(*key)
+        arr = _SEQ_CACHE[key] = _ints(key, len(key), "seq_ids")
     return arr, len(key)
 
 
 def _ints(values: Sequence[int], n: int, name: str):
     if len(values) != n:
         raise ValueError(f"{name} must have {n} entries, got {len(values)}")
-    return (ctypes.c_int32 * max(n, 1))(*[int(v) for v in values])
+    v = [int(x) for x in values]
+    if v and not (-0x80000000 <= min(v) and max(v) <= 0x7FFFFFFF):  # ctypes would keep the low 32 bits
+        raise ValueError(f"{name}: {max(v, key=abs)} does not fit in 32 bits")
+    return (ctypes.c_int32 * max(n, 1))(*v)
 
 
 def query_sizes(cfg: StoreConfig) -> dict:
@@ -211,8 +214,7 @@ class Store:
             check(lib().puzzlekv_factorize_pages(self._h, None, None, -1, _stream(stream)))
             return
         n = len(pages)
-        seqs = (ctypes.c_int32 * max(n, 1))(*[int(b) for b, _ in pages])
-        pgs = (ctypes.c_int32 * max(n, 1))(*[int(p) for _, p in pages])
+        seqs, pgs = _ints([b for b, _ in pages], n, "pages"), _ints([p for _, p in pages], n, "pages")
         check(lib().puzzlekv_factorize_pages(self._h, seqs, pgs, n, _stream(stream)))
 
     def factorize_layer(self, seq: int, layer: int, k: torch.Tensor, v: torch.Tensor, background: bool = True,

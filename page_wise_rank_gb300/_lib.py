@@ -64,6 +64,17 @@ class Config(ctypes.Structure):
         ("rope_theta", ctypes.c_float)]
 
 
+class Int32(ctypes.c_int32):
+    """An int argument of the C ABI.  ctypes keeps the low 32 bits of a longer number, which may well be a valid one;
+    the nearest int32 instead is out of range wherever the number itself is, and refused there."""
+
+    @classmethod
+    def from_param(cls, v):
+        if isinstance(v, ctypes.c_int32):
+            return v
+        return ctypes.c_int32(v if -0x80000000 <= v <= 0x7FFFFFFF else (0x7FFFFFFF if v > 0 else -0x80000000))
+
+
 _lib = None
 
 
@@ -113,7 +124,7 @@ def lib() -> ctypes.CDLL:
     }
     for name, (args, res) in sig.items():
         f = getattr(L, name)
-        f.argtypes = args
+        f.argtypes = [Int32 if a is i32 else a for a in args]
         f.restype = res
     _lib = L
     return L

@@ -92,8 +92,8 @@ puzzlekv_status validate_config(const puzzlekv_config *c) {
     if (c->max_batch > (1 << 16) || c->max_tokens_per_seq > (1 << 24) || c->num_layers > 255)
         return fail(PUZZLEKV_ERR_UNSUPPORTED, "max_batch, max_tokens_per_seq or num_layers too large");
     int P = c->page_size;
-    int sink_pages = (c->sink_tokens + P - 1) / P;
-    int ring = (c->recent_tokens + P - 1) / P + 2;
+    const long sink_pages = ((long)c->sink_tokens + P - 1) / P;
+    const long ring = ((long)c->recent_tokens + P - 1) / P + 2;
     if (sink_pages + ring > MAX_DENSE_PAGES)
         return fail(PUZZLEKV_ERR_UNSUPPORTED, "sink + window span more than %d dense pages", MAX_DENSE_PAGES - 2);
     int n_pg = (c->max_tokens_per_seq + P - 1) / P;
