@@ -387,7 +387,8 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t la
  *            in stores with rope_theta > 0; queries already rotated).  An
  *            infinity or NaN in a token's row reaches the outputs of the tokens
  *            that see it (a value's, its column alone), and no others.
- *   out:     device, [N][num_q_heads][head_dim] in kv_dtype.
+ *   out:     device, [N][num_q_heads][head_dim] in kv_dtype; may be q itself, and
+ *            overlaps no other buffer of the call.
  *   seq_ids, counts: host, B distinct slots, empty ones included, and the
  *            number of new tokens of each, 0 or more; at most
  *            max_tokens_per_seq with the cached ones.
@@ -425,7 +426,8 @@ puzzlekv_status puzzlekv_append_chunk(puzzlekv_store *store, int32_t layer, cons
  * counts[i] - 1 of each listed sequence, factorized pages rebuilt as L R
  * (rounded once to kv_dtype), dense rows as stored, keys of stores with
  * rope_theta > 0 turned at their positions.
- *   k, v: device, [N][num_kv_heads][head_dim] in kv_dtype, N = sum of counts.
+ *   k, v: device, [N][num_kv_heads][head_dim] in kv_dtype, N = sum of counts,
+ *         without overlap.
  */
 puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *store, int32_t layer, const int32_t *seq_ids,
                                      const int32_t *starts, const int32_t *counts, int32_t B, void *k, void *v,

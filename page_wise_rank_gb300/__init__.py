@@ -343,6 +343,7 @@ class Store:
         """Attention of a chunk of new tokens per sequence over the cache and, causally, the
         chunk (§3.3 ④): q [N, Hq, d], k, v [N, H, d], N = sum(counts), sequences one after another.
         Returns out [N, Hq, d] in kv_dtype; the store is unchanged (append_chunk adds the chunk).
+        `out` may be q itself, and shares no memory with another of the tensors.
         `workspace` (uint8, of chunk_workspace's size) is allocated if not given."""
         c = self.cfg
         ids, B = _seq_ids(seq_ids)

@@ -340,6 +340,12 @@ size_t gather_bytes(const Layout &y, const LeavePlan &lp) {
     return 2 * up256(rows * y.H * y.d * y.esz);
 }
 
+// Do [a, a + na) and [b, b + nb) share a byte?
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), z = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < z + nb && z < x + na;
+}
+
 puzzlekv_status check_work(const void *work, size_t have, size_t need) {
     if (need == 0) return PUZZLEKV_OK;
     if (!work || (reinterpret_cast<uintptr_t>(work) & 255u) != 0)
@@ -390,6 +396,16 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
         if (pl.nseq == 0) return PUZZLEKV_OK;
         st = check_work(work, work_bytes, pl.bytes);
         if (st != PUZZLEKV_OK) return st;
+        // A row of out is written after its own row of q is read, but beside reads
+        // of the others and of the chunk's keys and values.
+        size_t tokens = 0;
+        for (int i = 0; i < B; ++i) tokens += counts[i];
+        const size_t qb = tokens * y.Hq * y.d * y.esz, kb = tokens * y.H * y.d * y.esz;
+        if (overlap(out, qb, k, kb) || overlap(out, qb, v, kb) || (out != q && overlap(out, qb, q, qb)))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "out must not overlap k, v or (unless it is q) q");
+        if (overlap(work, pl.bytes, q, qb) || overlap(work, pl.bytes, k, kb) || overlap(work, pl.bytes, v, kb) ||
+            overlap(work, pl.bytes, out, qb))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "the workspace must not overlap q, k, v or out");
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
         st = refuse_pending(s, strm);
         if (st != PUZZLEKV_OK) return st;
@@ -482,6 +498,9 @@ puzzlekv_status puzzlekv_append_chunk(puzzlekv_store *s, int32_t layer, const vo
         }
         if (off == 0) return PUZZLEKV_OK;
         st = check_work(work, work_bytes, need);
+        const size_t kb = (size_t)off * y.H * y.d * y.esz;
+        if (st == PUZZLEKV_OK && (overlap(work, need, k, kb) || overlap(work, need, v, kb)))
+            st = fail(PUZZLEKV_ERR_INVALID_ARG, "the workspace must not overlap k or v");
         if (st == PUZZLEKV_OK) st = refuse_capture(strm);
         if (st != PUZZLEKV_OK) return st;
         // a page converted in the background becomes factorized, or its ring
@@ -603,6 +622,8 @@ puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int
             off += counts[i];
         }
         if (off == 0) return PUZZLEKV_OK;
+        const size_t kb = (size_t)off * y.H * y.d * y.esz;
+        if (overlap(k, kb, v, kb)) return fail(PUZZLEKV_ERR_INVALID_ARG, "k and v must not overlap");
         rp.nseq = B;
         rp.k_out = static_cast<char *>(k);
         rp.v_out = static_cast<char *>(v);
