@@ -669,9 +669,10 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                     bulk_g2s(ring + (x % RING) * IMG, src + (size_t)k * IMG, IMG, &s.kv_full[x % RING]);
                 }
             }
-            if (!ok)  // copies still in flight land before the CTA ends
-                for (uint32_t k = x < RING ? 0 : x - RING; k < x; ++k)
-                    mbar_wait_bounded(&s.kv_full[k % RING], (k / RING) & 1, nullptr);
+            // copies still in flight land before the CTA ends, also where another
+            // role gives up after the last of them was started
+            for (uint32_t k = x < RING ? 0 : x - RING; k < x; ++k)
+                mbar_wait_bounded(&s.kv_full[k % RING], (k / RING) & 1, nullptr);
         }
     }
     __syncwarp();
