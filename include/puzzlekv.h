@@ -505,6 +505,19 @@ puzzlekv_status puzzlekv_store_stats(const puzzlekv_store *store, int32_t seq, i
 puzzlekv_status puzzlekv_debug_fail_next_wait(puzzlekv_store *store, int32_t where, int64_t wait_ns);
 
 /*
+ * The same hook for the chunk and sequence calls (bf16 stores; fp32 ones for
+ * where = 5): in the next launch of one kernel, the first barrier that its first
+ * CTA fills expects 16 bytes that no copy delivers, and the launch's waits run out
+ * after wait_ns.  where = 1: attention of few tokens, 2: staging of the operand
+ * images, 3: attention over them, 4: row reads, 5: sequence copies; 0 clears a
+ * pending request.  The CTA lets its copies land and ends; the launch's outputs
+ * (5: the destinations' content) are undefined, the next
+ * puzzlekv_check_device_status returns PUZZLEKV_ERR_DEVICE_TIMEOUT, and later
+ * calls are right.
+ */
+puzzlekv_status puzzlekv_debug_fail_next_chunk_wait(puzzlekv_store *store, int32_t where, int64_t wait_ns);
+
+/*
  * Synchronise `stream`, read the device status word and clear it.  Returns
  * PUZZLEKV_ERR_NOT_CONVERGED if an eigensolve hit its iteration cap since the last
  * check, PUZZLEKV_ERR_DEVICE_TIMEOUT if a kernel's bounded wait ran out.

@@ -449,6 +449,11 @@ class Store:
         (1 = a unit copy, 2 = the split merge) runs out after wait_ns (see include/puzzlekv.h)."""
         check(lib().puzzlekv_debug_fail_next_wait(self._h, int(where), int(wait_ns)))
 
+    def debug_fail_next_chunk_wait(self, where: int, wait_ns: int = 2_000_000) -> None:
+        """The same hook for the chunk and sequence calls: 1 few tokens, 2 staging, 3 attention over the images,
+        4 row reads, 5 sequence copies (see include/puzzlekv.h)."""
+        check(lib().puzzlekv_debug_fail_next_chunk_wait(self._h, int(where), int(wait_ns)))
+
     def check_device_status(self, stream=None) -> int:
         """Synchronise and return the status code (raises nothing; OK = 0)."""
         st = lib().puzzlekv_check_device_status(self._h, _stream(stream))

@@ -43,6 +43,7 @@ EXPORTED = (
     "puzzlekv_truncate_sequences",
     "puzzlekv_store_stats",
     "puzzlekv_debug_fail_next_wait",
+    "puzzlekv_debug_fail_next_chunk_wait",
     "puzzlekv_check_device_status",
     "puzzlekv_factorize_counters",
     "puzzlekv_classify_pages",
@@ -116,6 +117,7 @@ def lib() -> ctypes.CDLL:
         "puzzlekv_truncate_sequences": ([vp, i32p, i32p, i32, vp], i32),
         "puzzlekv_store_stats": ([vp, i32, i32, i32p, i64p, i64p, i64p], i32),
         "puzzlekv_debug_fail_next_wait": ([vp, i32, i64], i32),
+        "puzzlekv_debug_fail_next_chunk_wait": ([vp, i32, i64], i32),
         "puzzlekv_check_device_status": ([vp, vp], i32),
         "puzzlekv_factorize_counters": ([vp, vp, i64p, i64p], i32),
         "puzzlekv_classify_pages": ([i32, i32, i32, i32, i32p, i32], i32),

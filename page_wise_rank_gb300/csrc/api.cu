@@ -908,6 +908,18 @@ puzzlekv_status puzzlekv_debug_fail_next_wait(puzzlekv_store *s, int32_t where, 
     return PUZZLEKV_OK;
 }
 
+puzzlekv_status puzzlekv_debug_fail_next_chunk_wait(puzzlekv_store *s, int32_t where, int64_t wait_ns) {
+    if (!s) return fail(PUZZLEKV_ERR_INVALID_ARG, "store is NULL");
+    if (where < FAIL_NONE || where > FAIL_COPY) return fail(PUZZLEKV_ERR_INVALID_ARG, "where must be in [0, 5] (got %d)", where);
+    if (wait_ns < 1000 || wait_ns > (int64_t)1000000000)
+        return fail(PUZZLEKV_ERR_INVALID_ARG, "wait_ns must be in [1e3, 1e9] (got %lld)", (long long)wait_ns);
+    if (s->y.dtype != 1 && where != FAIL_NONE && where != FAIL_COPY)
+        return fail(PUZZLEKV_ERR_UNSUPPORTED, "fp32 stores wait in sequence copies only");
+    s->fail_chunk = where;
+    s->fail_chunk_ns = (uint64_t)wait_ns;
+    return PUZZLEKV_OK;
+}
+
 puzzlekv_status puzzlekv_check_device_status(puzzlekv_store *s, void *stream) {
     if (!s) return fail(PUZZLEKV_ERR_INVALID_ARG, "store is NULL");
     cudaStream_t strm = static_cast<cudaStream_t>(stream);

@@ -94,6 +94,16 @@ puzzlekv_status check_chunk(const puzzlekv_store *s, int32_t layer, const int32_
     return PUZZLEKV_OK;
 }
 
+// The test hook's request for this kernel, if there is one: consumed by the launch.
+WaitHook take_hook(puzzlekv_store *s, int kernel) {
+    WaitHook h;
+    if (s->fail_chunk != kernel) return h;
+    h.inject = 1;
+    h.wait_ns = s->fail_chunk_ns;
+    s->fail_chunk = FAIL_NONE;
+    return h;
+}
+
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // First dense page past the sink of a T-token sequence (pages [sink, it) are factorized).
@@ -426,6 +436,8 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
             pl.f.scales = pl.g.scales;
             pl.f.partials = reinterpret_cast<float *>(w + pl.flash_parts);
             pl.f.status = status_ptr(s);
+            pl.g.hook = take_hook(s, FAIL_STAGE);
+            pl.f.hook = take_hook(s, FAIL_FLASH);
             e = launch_stage(pl.g, s->num_sms, strm);
             if (e == cudaSuccess) e = launch_flash(pl.f, y.d, strm);
         }
@@ -442,6 +454,7 @@ puzzlekv_status puzzlekv_chunk_attention(puzzlekv_store *s, int32_t layer, const
             pl.s.out = a.out;
             pl.s.partials = a.partials;
             pl.s.status = status_ptr(s);
+            pl.s.hook = take_hook(s, FAIL_SMALL);
             e = launch_small(pl.s, strm);
         }
         if (pl.r.nseq && e == cudaSuccess) {
@@ -634,6 +647,7 @@ puzzlekv_status puzzlekv_read_tokens(puzzlekv_store *s, int32_t layer, const int
         if (st != PUZZLEKV_OK) return st;
         wait_conversions(s, strm, seq_ids, lens, B);
         s->after_decode = false;
+        rp.hook = take_hook(s, FAIL_READ);
         const cudaError_t e = launch_read(rp, s->num_sms, strm);
         if (e != cudaSuccess) return cuda_fail(e, "row read launch");
         return PUZZLEKV_OK;
@@ -747,6 +761,7 @@ puzzlekv_status puzzlekv_copy_sequences(puzzlekv_store *s, const int32_t *src_id
             }
         wait_conversions(s, strm, nullptr, nullptr, 0, true);
         s->after_decode = false;
+        p.hook = take_hook(s, FAIL_COPY);
         const cudaError_t e = launch_copy(p, s->num_sms, strm);
         if (e != cudaSuccess) return cuda_fail(e, "sequence copy launch");
         for (int i = 0; i < p.npair; ++i)

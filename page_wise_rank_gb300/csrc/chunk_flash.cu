@@ -67,18 +67,18 @@ struct FlashShared {
 };
 
 // Bounded wait of one role; when it gives up, or another role has, every role leaves.
-__device__ __forceinline__ bool role_wait(FlashShared &s, uint64_t *bar, uint32_t parity, int *status) {
+__device__ __forceinline__ bool role_wait(FlashShared &s, uint64_t *bar, uint32_t parity, const FlashParams &p) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15) == 0) {
             if (s.failed) return false;
-            if (global_ns() - t0 > WAIT_NS) break;
+            if (global_ns() - t0 > p.hook.limit()) break;
         }
     }
     s.failed = 1;
-    atomicOr(status + STATUS_TIMEOUT, 1);
+    atomicOr(p.status + STATUS_TIMEOUT, 1);
     return false;
 }
 
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
         const StageItem it = its[buf] = StageItem(p, item);
         BlockPages(y, NP, it.blk * NP, it.fw, it.kv)
-            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf]);
+            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf], item == 0 ? p.hook.extra() : 0);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     grid_launch_dependents();  // the attention may be set up
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
             bad = __syncthreads_or(fetch_dense<P, D>(y, bp, p.dense_pool, it.kv ? p.v_new : p.k_new, p.off[it.i], p.layer, it.b,
                                                      it.h, it.kv, it.T0, it.T1, pages, bl.page_bytes));
         if (bp.lo < bp.hi) {
-            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
+            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status, p.hook.limit()) ? 1 : 0) != 0;
             if (!ok) {  // let the copies land, then leave the images as they are
                 if (tid == 0) {
                     mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 const int ev = (int)sc.y;
                 if (blk + 1 < pc.cb1) sc = scales[blk + 1];
                 // a warp leaves as one: tensor-memory accesses are whole-warp operations
-                if (!(ok = __all_sync(0xffffffffu, role_wait(s, &s.s_full[t], s_phase, p.status)))) break;
+                if (!(ok = __all_sync(0xffffffffu, role_wait(s, &s.s_full[t], s_phase, p)))) break;
                 s_phase ^= 1;
                 tc_fence_after();
                 uint32_t x[4][32];
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 tc_fence_before();
                 mbar_arrive(&s.p_full[t]);
             }
-            if (!ok || !__all_sync(0xffffffffu, role_wait(s, &s.o_full[t], o_phase, p.status))) break;
+            if (!ok || !__all_sync(0xffffffffu, role_wait(s, &s.o_full[t], o_phase, p))) break;
             o_phase ^= 1;
             tc_fence_after();
             const float unit = pow2i(E);
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
             constexpr uint32_t ID_S = tc_idesc_f16(128, FLASH_KEYS), ID_O = tc_idesc_f16(128, D);
             uint32_t x = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
             bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, role_wait(s, bar, parity, p.status)) != 0; };
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, role_wait(s, bar, parity, p)) != 0; };
             auto full = [&](uint32_t n) { return wait(&s.kv_full[n % RING], (n / RING) & 1); };
             auto scores = [&](int t, uint32_t n) {
                 const uint64_t a = dq + t * (IMG >> 4), b = dr + (n % RING) * (IMG >> 4);
@@ -663,9 +663,9 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
             while (ok && pc.next()) {
                 const char *src = p.images + (size_t)pc.image(pc.cb0) * (2 * IMG);
                 for (int k = 0; k < 2 * (pc.cb1 - pc.cb0) && ok; ++k, ++x) {
-                    ok = role_wait(s, &s.kv_empty[x % RING], ((x / RING) & 1) ^ 1, p.status);
+                    ok = role_wait(s, &s.kv_empty[x % RING], ((x / RING) & 1) ^ 1, p);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&s.kv_full[x % RING], IMG);
+                    mbar_arrive_expect_tx(&s.kv_full[x % RING], IMG + (x == 0 ? p.hook.extra() : 0));
                     bulk_g2s(ring + (x % RING) * IMG, src + (size_t)k * IMG, IMG, &s.kv_full[x % RING]);
                 }
             }

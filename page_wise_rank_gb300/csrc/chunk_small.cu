@@ -360,16 +360,17 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
         const int u = pg + k * PG;
         if (u >= units) return true;
         const int sl = slot_of(k);
-        if (k >= SPG && !mbar_wait_bounded(&sh.empty[sl], (k / SPG - 1) & 1, p.status)) return false;
+        if (k >= SPG && !mbar_wait_bounded(&sh.empty[sl], (k / SPG - 1) & 1, p.status, p.hook.limit())) return false;
         int page, row;
         unit(u, page, row);
         unsigned char *dst = sm + (size_t)sl * p.unit_bytes;
+        const uint32_t extra = u == 0 ? p.hook.extra() : 0;
         if (row < 0) {
-            mbar_arrive_expect_tx(&sh.full[sl], rec_bytes);
+            mbar_arrive_expect_tx(&sh.full[sl], rec_bytes + extra);
             bulk_g2s(dst, records + (size_t)page * rec_bytes, rec_bytes, &sh.full[sl]);
         } else {
             const char *src = dense + y.dense_slot(page) * slot_bytes + (size_t)row * D * 2;
-            mbar_arrive_expect_tx(&sh.full[sl], 2 * HALF);
+            mbar_arrive_expect_tx(&sh.full[sl], 2 * HALF + extra);
             bulk_g2s(dst, src, HALF, &sh.full[sl]);
             bulk_g2s(dst + HALF, src + y.dense_half_bytes, HALF, &sh.full[sl]);
         }
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(32 * SMALL_WARPS, 1) small_kernel(const SmallP
         for (int k = 0; pg + k * PG < units; ++k) {
             const int sl = slot_of(k);
             // a warp leaves as one
-            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[sl], (k / SPG) & 1, p.status)) != 0;
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[sl], (k / SPG) & 1, p.status, p.hook.limit())) != 0;
             if (!ok) break;
             // the slot of the unit before is free, or nearly: the next copy goes there
             if (leader && k > 0 && (ok = issue(issued))) ++issued;

@@ -55,9 +55,6 @@ __device__ __forceinline__ uint64_t global_ns() {
     return t;
 }
 
-// Longest time any spin-wait of the library waits before it gives up.
-constexpr uint64_t WAIT_NS = 1000000000ull;
-
 // Wait for phase `parity` of `bar` to complete, giving up after `limit_ns`
 // of polling (each try_wait itself suspends for a short while).  On give-up
 // the device status word records a timeout and false is returned.

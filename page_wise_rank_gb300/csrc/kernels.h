@@ -102,6 +102,19 @@ struct AppendParams {
     int conv_page[MAX_CALL_BATCH]; // page converted by this call, or -1
 };
 
+// Failure-path test hook of the chunk kernels: with `inject` set, the first
+// barrier that the launch's first CTA fills expects 16 bytes that no copy
+// delivers, and waits give up after `wait_ns` (0: the library's limit).
+enum { FAIL_NONE = 0, FAIL_SMALL = 1, FAIL_STAGE = 2, FAIL_FLASH = 3, FAIL_READ = 4, FAIL_COPY = 5 };
+struct WaitHook {
+    int inject = 0;
+    uint64_t wait_ns = 0;
+#if defined(__CUDACC__)
+    __device__ __forceinline__ uint32_t extra() const { return inject && blockIdx.x == 0 && blockIdx.y == 0 ? 16u : 0u; }
+    __device__ __forceinline__ uint64_t limit() const { return wait_ns ? wait_ns : WAIT_NS; }
+#endif
+};
+
 // Rows of the cache of a list of sequences, as attention sees them: row t of
 // call entry i comes from the store for t < T[i] (factorized pages rebuilt as
 // L R, by launch_read with keys stored before RoPE turned) and from the chunk
@@ -121,6 +134,7 @@ struct RowsParams {
     int off[MAX_CALL_BATCH], coff[MAX_CALL_BATCH];
     int fw[MAX_CALL_BATCH];  // launch_read: page after the last factorized one
     int page_off[MAX_CALL_BATCH + 1];  // pages touched by the entries before (filled by the launcher)
+    WaitHook hook;
 };
 
 // Chunk append: rows T[i] .. T[i] + n[i] - 1 of entry i, from k / v ([sum
@@ -170,6 +184,7 @@ struct CopyParams {
     // filled by the launcher
     int max_upto, tile;
     unsigned long long any_slots;
+    WaitHook hook;
 };
 
 // Attention of a chunk of queries over rows laid out densely, and the merge
@@ -214,6 +229,7 @@ struct StageParams {
     int seqs[MAX_CALL_BATCH], T[MAX_CALL_BATCH], n[MAX_CALL_BATCH], off[MAX_CALL_BATCH];
     int fw[MAX_CALL_BATCH];  // page after the last factorized one (pages [sink_pages, fw) are)
     int blk_off[MAX_CALL_BATCH + 1];
+    WaitHook hook;
 };
 
 // The query rows of (entry, KV head) are cut into pairs of 128-row tiles; pair
@@ -238,6 +254,7 @@ struct FlashParams {
         int i, h, pair, b0;
         long long units;
     } share[FLASH_MAX_CTAS];
+    WaitHook hook;
 };
 
 // Blocks that pair p of an entry of T cached and n new tokens attends.
@@ -268,6 +285,7 @@ struct SmallParams {
     int boff[MAX_CALL_BATCH + 1];  // first bound of each entry; split numbers run boff[i] - i ..
     long long poff[MAX_CALL_BATCH];
     int bounds[SMALL_BOUNDS];
+    WaitHook hook;
 };
 // Shared memory that a launch for these entries would take (0: they do not fit).
 size_t small_smem_bytes(const Layout &y, int most_tokens);

@@ -54,6 +54,7 @@ constexpr int MAX_CALL_BATCH = 64;  // sequences per append / attention call
 constexpr int STATUS_WORDS = 16;    // int32 status words at the workspace start
 constexpr int STATUS_NOT_CONVERGED = 0;
 constexpr int STATUS_TIMEOUT = 1;
+constexpr uint64_t WAIT_NS = 1000000000ull;  // longest time any spin-wait of the library waits before it gives up
 constexpr int STATUS_JOBS = 2;      // uint64 at words 2-3: page jobs factorized
 constexpr int STATUS_ROTATIONS = 4; // uint64 at words 4-5: QL rotations those jobs applied (rank > P / 2)
 

@@ -51,15 +51,15 @@ struct BlockPages {
         hi = max(0, min(pages, fw - pg0));
         if (hi < lo) hi = lo;
     }
-    // One thread: start the copies of the factorized pages' parts.
+    // One thread: start the copies of the factorized pages' parts (`extra`: bytes expected in vain).
     template <bool Q4>
     __device__ __forceinline__ void fetch(const Layout &y, const BlockLayout &bl, const char *factor_pool, int layer, int b, int h,
-                                          int kv, unsigned char *buf, uint64_t *bar) const {
+                                          int kv, unsigned char *buf, uint64_t *bar, uint32_t extra) const {
         if (lo == hi) return;
         const size_t off = kv ? (Q4 ? y.q_off_V : y.off_LV) : 0;
         const uint32_t part = (uint32_t)((kv ? (Q4 ? y.q_off_sRK : y.rec_bytes) : (Q4 ? y.q_off_V : y.off_LV)) - off);
         const uint32_t tail = Q4 ? (uint32_t)(y.rec_bytes - y.q_off_sRK) : 0;
-        mbar_arrive_expect_tx(bar, (uint32_t)(hi - lo) * (part + tail));
+        mbar_arrive_expect_tx(bar, (uint32_t)(hi - lo) * (part + tail) + extra);
         const char *src = factor_pool + y.record_offset(layer, b, h, pg0 + lo);
         for (int s = lo; s < hi; ++s, src += y.rec_bytes) {
             bulk_g2s(buf + s * bl.fetch_bytes, src + off, part, bar);

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
     auto fetch = [&](int item, int buf) {  // one thread: an item's place and its factors
         const ReadItem it = its[buf] = ReadItem(p, item, NP);
         BlockPages(y, NP, it.pg0, it.fw, it.kv)
-            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf]);
+            .fetch<Q4>(y, bl, p.factor_pool, p.layer, it.b, it.h, it.kv, buffer(buf), &bars[buf], item == 0 ? p.hook.extra() : 0);
     };
     if (tid == 0 && (int)blockIdx.x < items) fetch(blockIdx.x, 0);
     __syncthreads();
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) read_kernel(const RowsParams
             __syncthreads();
         }
         if (bp.lo < bp.hi) {
-            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status) ? 1 : 0) != 0;
+            const bool ok = __syncthreads_and(mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, p.status, p.hook.limit()) ? 1 : 0) != 0;
             if (!ok) {
                 if (tid == 0) {
                     mbar_wait_bounded(&bars[buf], (phase >> buf) & 1, nullptr);

@@ -100,12 +100,12 @@ __global__ void __launch_bounds__(32) copy_sequences_kernel(const CopyParams p) 
         if (tx == 0) continue;
         // the previous tile's stores have read the stage
         asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        mbar_arrive_expect_tx(&bar, tx);
+        mbar_arrive_expect_tx(&bar, tx + (tile == 0 ? p.hook.extra() : 0));
         for (int j = 0; j < p.nsrc; ++j) {
             const uint32_t nb = bytes_of(j);
             if (nb) bulk_g2s(stage + (size_t)j * p.tile, pool + base + (size_t)p.src[j] * stride + off, nb, &bar);
         }
-        if (!mbar_wait_bounded(&bar, phase, p.status)) {  // give up: let the copies land, write nothing more
+        if (!mbar_wait_bounded(&bar, phase, p.status, p.hook.limit())) {  // give up: let the copies land, write nothing more
             mbar_wait_bounded(&bar, phase, nullptr);
             break;
         }

@@ -50,6 +50,8 @@ struct puzzlekv_store {
     bool after_decode = false;   // the store's latest launch was a decode launch
     int fail_next = 0;           // failure-path test hook for the next decode launch (0 = off)
     uint64_t fail_wait_ns = 0;   // its waits' limit
+    int fail_chunk = 0;          // the same for the next launch of one chunk kernel (FAIL_* in kernels.h)
+    uint64_t fail_chunk_ns = 0;
     int num_sms;
     // Batched conversions run on an internal low-priority stream.  A batch's
     // factor records are first read when one of its pages becomes
