@@ -668,7 +668,8 @@ puzzlekv_status puzzlekv_load_factors(puzzlekv_store *s, int32_t layer, int32_t 
             return fail(PUZZLEKV_ERR_INVALID_ARG, "pages [%d, %d + %d): sequence %d has complete pages [%d, %d) past its sink",
                         page0, page0, n, seq, y.sink_pages, complete);
         if (n == 0) return PUZZLEKV_OK;
-        if (!LK || !RK || !LV || !RV) return fail(PUZZLEKV_ERR_INVALID_ARG, "factors must be non-NULL");
+        if (!LK || !RK || !LV || !RV || !aligned16(LK) || !aligned16(RK) || !aligned16(LV) || !aligned16(RV))
+            return fail(PUZZLEKV_ERR_INVALID_ARG, "factors must be non-NULL and 16-byte aligned");
         cudaStream_t strm = static_cast<cudaStream_t>(stream);
         st = refuse_capture(strm);
         if (st != PUZZLEKV_OK) return st;

@@ -59,3 +59,36 @@ def test_overlaps_are_refused(pkv):
                                        need, stream) != 0
         assert "overlap" in pkv.last_error()
     assert store.stats(0, 0)["length"] == 700
+
+
+def test_misaligned_buffers_are_refused(pkv):
+    """Every device pointer of the chunk calls off by one element or byte: refused before anything is launched."""
+    cfg = make_cfg(pkv, num_layers=1)
+    store, _ = filled(pkv, cfg, [700, 0, 0, 0])
+    L, B = pkv.lib(), (ctypes.c_int32 * 1)(0)
+    n = (ctypes.c_int32 * 1)(3)
+    buf = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    work = torch.zeros(store.chunk_workspace(0, [0], [3])["attention"], dtype=torch.uint8, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    at = lambda i, off: ctypes.c_void_p(buf.data_ptr() + (i << 17) + off)
+    before = store.factor_pool.clone()
+
+    def attend(p):
+        return L.puzzlekv_chunk_attention(store.handle, 0, *p, B, n, 1, ctypes.c_void_p(work.data_ptr()), work.numel(), stream)
+
+    def append(p):
+        return L.puzzlekv_append_chunk(store.handle, 0, *p, B, n, 1, None, 0, stream)
+
+    def read(p):
+        return L.puzzlekv_read_tokens(store.handle, 0, B, B, n, 1, *p, stream)
+
+    def load(p):
+        return L.puzzlekv_load_factors(store.handle, 0, 0, 2, 1, *p, stream)
+
+    for call, count in ((attend, 4), (append, 2), (read, 2), (load, 4)):
+        for i in range(count):
+            for off in (1, 2, 8):
+                assert call([at(j, off if j == i else 0) for j in range(count)]) == pkv._lib.ERR_INVALID_ARG
+                assert "aligned" in pkv.last_error()
+    assert torch.equal(before, store.factor_pool) and store.stats(0, 0)["length"] == 700
+    assert load([at(j, 0) for j in range(4)]) == 0 and attend([at(j, 0) for j in range(4)]) == 0
