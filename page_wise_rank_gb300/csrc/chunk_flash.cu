@@ -150,7 +150,10 @@ __device__ __forceinline__ float finite_abs(float x) {
 // block: 11 bits against bf16's 8, because a key's rounding moves its score,
 // and the scores' errors, unlike the output's rounding, grow with |s|.
 // (Rebuilt keys and values in bf16 left 6e-3 of the output's norm at 32K tokens,
-// 3.5 times the output's own rounding.)
+// 3.5 times the output's own rounding; fp16 leaves 1.8e-3 there and 1.9e-3 at
+// 128K, the bf16 output's own rounding being 1.7e-3.)  The powers follow each
+// block's largest element, so ordinary spreads inside a block (columns of unlike
+// sizes) lose nothing; a value's power is a multiple of four (value_exponent).
 //
 // HBM-bound: 47 % of the image bytes are read, all are written.  Every step of
 // an item is short and waits on the one before, so CTAs stay and loop over
@@ -365,8 +368,8 @@ __global__ void __launch_bounds__(STAGE_THREADS, 2) stage_kernel(const StagePara
 //
 // Bound by the softmax and the products together: a unit of 2 x 128 x 128 takes
 // 3,180 cycles, its products 2,048, each tile's softmax 1,550 (exponentials and
-// packing 975 of them).  2,048 tokens over 30K, 32 / 8 heads: 670 us, 1.6 PFLOP/s,
-// tensor cores active 70 %.  Slower: two threads to a row (the exchange of maxima
+// packing 975 of them).  2,048 tokens over 30K, 32 / 8 heads: 670 to 690 us, 1.55
+// PFLOP/s, tensor cores active 70 %.  Slower: two threads to a row (the exchange of maxima
 // costs what the halves save), a warp per tile for the products (they interleave),
 // a share of the exponentials as polynomials (the special-function unit is not the
 // bound).
