@@ -389,7 +389,8 @@ puzzlekv_status puzzlekv_chunk_workspace(const puzzlekv_store *store, int32_t la
  *     against bf16's 8: a key element down to 2^-26 of the largest in its block
  *     of 128 positions, a value element to 2^-25, a query element to 2^-26 of
  *     its row's, a weight to 2^-17 of its row's largest.  Smaller ones keep a
- *     step of 2^-36, 2^-35, 2^-36 and 2^-27 of those.  The output is then off by
+ *     step of 2^-36, 2^-35, 2^-36 and 2^-27 of those.  Beside values 2^60 times
+ *     larger in earlier blocks, a block's weights lose bits.  The output is off by
  *     about a tenth more than its own rounding (0.0019 of its norm at 128K tokens).
  *   q:       device, [N][num_q_heads][head_dim] in kv_dtype, N = sum of counts,
  *            the sequences' tokens one after another in list order;
