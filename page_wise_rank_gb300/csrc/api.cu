@@ -41,6 +41,7 @@ puzzlekv_status pkv::fail(puzzlekv_status st, const char *fmt, ...) {
 }
 
 puzzlekv_status pkv::cuda_fail(cudaError_t e, const char *what) {
+    (void)cudaGetLastError();  // reported here: not again by the next call's launch check
     return fail(PUZZLEKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 

@@ -495,10 +495,11 @@ __global__ void __launch_bounds__(FLASH_THREADS, 1) flash_kernel(const FlashPara
                 // The reference m moves only when a score exceeds it by 2^8, so O is
                 // rescaled rarely.  The weights are 2^7 times 2^(s - m), up to 2^15: fp16
                 // holds them in full down to 2^-21 of the reference's and to a step
-                // of 2^-31 below, so that a long tail still counts.  A value block whose power is above E, or two steps below,
-                // rescales it as well, exactly: a block's weights are never
-                // more than one step short of their bits.  (A power 2^60 below
-                // the largest stays short: O, at most 2^30 T units, must not overflow.)
+                // of 2^-31 below, so that a long tail still counts.  A value block
+                // whose power is above E, or two steps below, rescales O as well,
+                // exactly: a block's weights are never more than one step short of
+                // their bits.  (A power 2^60 below the largest stays short: O, at
+                // most 2^30 T units, must not overflow.)
                 float f = 1.f;
                 if (blk == pc.cb0) {
                     m = mx;
